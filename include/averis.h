@@ -391,6 +391,165 @@ avr_status averis_moe_linear_dgrad(const void* D, avr_dtype dt, int64_t l_cap, c
                                    avr_stream stream);
 
 /* -------------------------------------------------------------------------
+ * Routing of a mixture of experts: the router, the sort of tokens by expert,
+ * dispatch to the experts' buffer and combine, with their gradients.  The
+ * pages train an MoE model [Abs] and say nothing of its routing; these calls
+ * make and read the buffer of the *_moe_* calls: expert e's tokens are rows
+ * [o_e, o_e + counts[e]), o_0 = 0, o_{e+1} = o_e + counts[e] rounded up to 128.
+ *
+ * T tokens (T >= 0, T k < 2^31; T = 0 is a no-op, but moe_sort writes its
+ * counts), k slots a token
+ * (1 <= k <= 32), E experts (1 <= E <= 1024, k <= E for the router), H
+ * features (H % 8 == 0).  ids, row, weights and their gradients are [T, k];
+ * a negative id or row is a slot without an expert: it takes no row, adds
+ * nothing and its gradient is 0, whatever its weight holds.  Buffers have
+ * l_cap rows (a multiple of 128); rows that hold no token are neither read
+ * nor written.  An id >= E or a row >= l_cap latches AVR_ERR_INVALID_ARG and
+ * counts as negative.  Sums in fp32, slots in ascending order: the same inputs give
+ * the same bits.  ws: moe_route_workspace_size(T, k, E) bytes covers all of
+ * them (a workspace of any other call of this library that is as large does too).
+ * ------------------------------------------------------------------------- */
+size_t moe_route_workspace_size(int64_t T, int k, int E);
+
+/* The k largest of each token's E logits, in descending order (ties: the
+ * lower index first; -inf is never chosen; slots left over get id -1, weight
+ * 0), and their softmax weights: over the k chosen (norm = 1) or over all E
+ * logits (norm = 0).  A NaN or +inf logit latches AVR_ERR_NONFINITE and
+ * leaves its token without experts.  Launches 1 kernel. */
+avr_status moe_route(const void* logits, avr_dtype lt, int64_t T, int E, int k, int norm, int32_t* ids,
+                     float* weights, void* ws, size_t ws_bytes, avr_stream stream);
+
+/* Gradient of the weights to the logits, dlogits [T, E] in lt, with s =
+ * sum_j dw_j w_j: at the chosen experts w_j (dw_j - s), 0 elsewhere (norm =
+ * 1; logits are not read and may be NULL), or p_e (dw_e - s) with the softmax
+ * p over all E and dw_e = 0 for the experts not chosen (norm = 0).  Launches
+ * 1 kernel. */
+avr_status moe_route_bwd(const void* logits, avr_dtype lt, int64_t T, int E, int k, int norm, const int32_t* ids,
+                         const float* weights, const float* dweights, void* dlogits, void* ws, size_t ws_bytes,
+                         avr_stream stream);
+
+/* Sort by expert: counts[e] = slots with id e, row[t, j] = o_e + the rank of
+ * slot (t, j) among its expert's in (t, j) order.  When the segments do not
+ * fit l_cap rows, AVR_ERR_INVALID_ARG is latched, counts are 0 and rows -1.
+ * l_cap >= T k + 127 min(E, T k), rounded down to 128, always fits.
+ * Launches 1 kernel (T k <= 1024) or 2. */
+avr_status moe_sort(const int32_t* ids, int64_t T, int k, int E, int64_t l_cap, int32_t* counts, int32_t* row,
+                    void* ws, size_t ws_bytes, avr_stream stream);
+
+/* Xp[row[t, j]] = X[t] (X [T, H] and Xp [l_cap, H] in xt), and its gradient
+ * dX[t] = sum_j dXp[row[t, j]].  Launches 1 kernel. */
+avr_status moe_dispatch(const void* X, avr_dtype xt, int64_t T, int k, int64_t H, const int32_t* row, int64_t l_cap,
+                        void* Xp, void* ws, size_t ws_bytes, avr_stream stream);
+avr_status moe_dispatch_bwd(const void* dXp, avr_dtype xt, int64_t T, int k, int64_t H, const int32_t* row,
+                            int64_t l_cap, void* dX, void* ws, size_t ws_bytes, avr_stream stream);
+
+/* Y[t] = sum_j weights[t, j] Yp[row[t, j]], and its gradients dYp[row[t, j]] =
+ * weights[t, j] dY[t], dweights[t, j] = <dY[t], Yp[row[t, j]]> (fp32).
+ * Launches 1 kernel. */
+avr_status moe_combine(const void* Yp, avr_dtype yt, int64_t T, int k, int64_t H, const int32_t* row,
+                       const float* weights, int64_t l_cap, void* Y, void* ws, size_t ws_bytes, avr_stream stream);
+avr_status moe_combine_bwd(const void* dY, const void* Yp, avr_dtype yt, int64_t T, int k, int64_t H,
+                           const int32_t* row, const float* weights, int64_t l_cap, void* dYp, float* dweights,
+                           void* ws, size_t ws_bytes, avr_stream stream);
+
+/* -------------------------------------------------------------------------
+ * 8-bit linear layer: E4M3 values with a scale for each block of 128
+ *
+ * A user's 8-bit arm beside the NVFP4 ones; the pages have no counterpart.
+ * A tensor [rows, K] has one scale 2^e per row and 128 elements of K (the last
+ * block of a row may be shorter); a weight has one per 128 x 128 block.  e is
+ * the smallest integer >= -127 with max|x| <= 448 * 2^e, and the code is
+ * E4M3(x 2^-e), nearest even: nothing saturates, and scaling itself is exact.
+ * A power of two is what the tensor cores apply (block_scale, E8M0), so a
+ * product needs no fp32 promotion between blocks.  A NaN or infinity latches
+ * AVR_ERR_NONFINITE (the outputs are then undefined).
+ * Sizes: m, n, K multiples of 16; l >= 0 tokens; all < 2^31.
+ * ------------------------------------------------------------------------- */
+
+/* codes  : rows * K bytes, row-major E4M3.
+ * scales : avr_fp8_scales_bytes(rows, K) bytes e + 127 in 512-byte atoms of
+ *          128 rows x 4 blocks: atom (r/128, c/4) at index (r/128) *
+ *          ceil(ceil(K/128)/4) + c/4, the byte of (r, c) at 16*(r%32) +
+ *          4*((r%128)/32) + c%4; bytes of no row or block are 0.
+ * value(r, k) = e4m3(code) * 2^(scale(r, k/128) - 127). */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t rows;
+  int64_t K;
+} avr_fp8;
+
+size_t avr_fp8_scales_bytes(int64_t rows, int64_t K);
+
+/* Workspace bytes of every call below without `moe` in its name: l tokens,
+ * m input and n output features. */
+size_t fp8_workspace_size(int64_t l, int64_t m, int64_t n);
+
+/* Q(X) of X [rows, K] along K.  Launches 1 kernel. */
+avr_status fp8_quant(const void* X, avr_dtype xt, int64_t rows, int64_t K, const avr_fp8* out, void* ws,
+                     size_t ws_bytes, avr_stream stream);
+
+/* Q(X^T) of X [l, K] along the tokens: out [K, L], L = l rounded up to 128
+ * (tokens l..L-1 are zeros).  Launches 1 kernel. */
+avr_status fp8_quant_t(const void* X, avr_dtype xt, int64_t l, int64_t K, const avr_fp8* out, void* ws,
+                       size_t ws_bytes, avr_stream stream);
+
+/* W [m, n] in 128 x 128 blocks for both products: w_fwd = Q(W)^T [n, m] and
+ * w_dgrad = Q(W) [m, n] (nullable), the same codes and scales.  Launches 1
+ * kernel. */
+avr_status fp8_quant_weight(const void* W, avr_dtype wt, int64_t m, int64_t n, const avr_fp8* w_fwd,
+                            const avr_fp8* w_dgrad, void* ws, size_t ws_bytes, avr_stream stream);
+
+/* Y [M, N] = A B^T of A = a [M, K] and B = b [N, K], fp32 accumulation, in yt
+ * (fp32 or bf16).  Launches 1 kernel. */
+avr_status fp8_gemm(const avr_fp8* a, const avr_fp8* b, void* Y, avr_dtype yt, void* ws, size_t ws_bytes,
+                    avr_stream stream);
+
+/* Y [l, n] = Q(X) Q(W), dX [l, m] = Q(D) Q(W)^T, dW [m, n] = Q(X^T) Q(D^T)^T
+ * (0 when l = 0).  Launch 2, 2 and 3 kernels. */
+avr_status fp8_linear_fwd(const void* X, avr_dtype xt, int64_t l, int64_t m, int64_t n, const avr_fp8* w_fwd, void* Y,
+                          avr_dtype yt, void* ws, size_t ws_bytes, avr_stream stream);
+avr_status fp8_linear_dgrad(const void* D, avr_dtype dt, int64_t l, int64_t m, int64_t n, const avr_fp8* w_dgrad,
+                            void* dX, avr_dtype xt, void* ws, size_t ws_bytes, avr_stream stream);
+avr_status fp8_linear_wgrad(const void* X, avr_dtype xt, const void* D, avr_dtype dt, int64_t l, int64_t m, int64_t n,
+                            void* dW, avr_dtype wt, void* ws, size_t ws_bytes, avr_stream stream);
+
+/* The same for E experts (1 <= E <= 1024) over the buffer of the *_moe_*
+ * calls (l_cap rows, counts on the device); m and n multiples of 128.  Rows
+ * that hold no token are neither read nor written.  Counts that do not fit
+ * l_cap latch AVR_ERR_INVALID_ARG and nothing is computed. */
+size_t fp8_moe_workspace_size(int64_t l_cap, int64_t m, int64_t n, int E);
+
+/* W [E][m][n] in 128 x 128 blocks, the experts stacked: w_fwd [E n, m],
+ * w_dgrad [E m, n] (nullable).  ws: fp8_moe_workspace_size(0, m, n, E).
+ * Launches 1 kernel. */
+avr_status fp8_moe_quant_weights(const void* W, avr_dtype wt, int E, int64_t m, int64_t n, const avr_fp8* w_fwd,
+                                 const avr_fp8* w_dgrad, void* ws, size_t ws_bytes, avr_stream stream);
+
+/* moe_dispatch and the quantizer in one pass: row row[t, j] of xq [l_cap, K]
+ * is Q(X[t]).  K % 128 == 0.  ws as the routing calls.  Launches 1 kernel. */
+avr_status fp8_moe_dispatch(const void* X, avr_dtype xt, int64_t T, int k, int64_t K, const int32_t* row,
+                            const avr_fp8* xq, void* ws, size_t ws_bytes, avr_stream stream);
+
+/* Y[r] = xq[r] W_e^T for the rows r of every expert e, w = the experts' [N, K]
+ * stacked (rows = E N).  Launches 2 kernels. */
+avr_status fp8_moe_gemm(const avr_fp8* xq, const int32_t* counts, int E, const avr_fp8* w, void* Y, avr_dtype yt,
+                        void* ws, size_t ws_bytes, avr_stream stream);
+
+/* Per expert: Y = Q(X) Q(W_e), dX = Q(D) Q(W_e)^T, dW [E][m][n] = Q(X^T)
+ * Q(D^T)^T over the expert's tokens (0 where it has none).  X [l_cap, m],
+ * D [l_cap, n].  Launch 3, 3 and 4 kernels. */
+avr_status fp8_moe_linear_fwd(const void* X, avr_dtype xt, int64_t l_cap, const int32_t* counts, int E, int64_t m,
+                              int64_t n, const avr_fp8* w_fwd, void* Y, avr_dtype yt, void* ws, size_t ws_bytes,
+                              avr_stream stream);
+avr_status fp8_moe_linear_dgrad(const void* D, avr_dtype dt, int64_t l_cap, const int32_t* counts, int E, int64_t m,
+                                int64_t n, const avr_fp8* w_dgrad, void* dX, avr_dtype xt, void* ws, size_t ws_bytes,
+                                avr_stream stream);
+avr_status fp8_moe_linear_wgrad(const void* X, avr_dtype xt, const void* D, avr_dtype dt, int64_t l_cap,
+                                const int32_t* counts, int E, int64_t m, int64_t n, void* dW, avr_dtype wt, void* ws,
+                                size_t ws_bytes, avr_stream stream);
+
+/* -------------------------------------------------------------------------
  * Diagnostics (used by the tests to pin the number formats on the device)
  * ------------------------------------------------------------------------- */
 

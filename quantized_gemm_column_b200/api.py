@@ -50,6 +50,10 @@ class avr_nvfp4(ctypes.Structure):
                 ("rows", _c_i64), ("K", _c_i64)]
 
 
+class avr_fp8(ctypes.Structure):
+    _fields_ = [("codes", _c_ptr), ("scales", _c_ptr), ("rows", _c_i64), ("K", _c_i64)]
+
+
 _SIGS = {
     "avr_nvfp4_scales_bytes": (_c_size, [_c_i64, _c_i64]),
     "averis_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
@@ -112,6 +116,40 @@ _SIGS = {
     "averis_probe_philox": (_c_int, [_c_u64, _c_u64, _c_u32, _c_i64, _c_ptr, _c_ptr]),
     "averis_probe_convert_sr": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_i64, _c_ptr]),
 }
+
+_c_fp8 = ctypes.POINTER(avr_fp8)
+_WS = [_c_ptr, _c_size, _c_ptr]                     # ws, ws_bytes, stream
+_PERM = [_c_int, _c_i64, _c_int, _c_i64, _c_ptr]    # dtype, T, k, H, row
+_SIGS.update({
+    "moe_route_workspace_size": (_c_size, [_c_i64, _c_int, _c_int]),
+    "moe_route": (_c_int, [_c_ptr, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_ptr, _c_ptr] + _WS),
+    "moe_route_bwd": (_c_int, [_c_ptr, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr]
+                      + _WS),
+    "moe_sort": (_c_int, [_c_ptr, _c_i64, _c_int, _c_int, _c_i64, _c_ptr, _c_ptr] + _WS),
+    "moe_dispatch": (_c_int, [_c_ptr] + _PERM + [_c_i64, _c_ptr] + _WS),
+    "moe_dispatch_bwd": (_c_int, [_c_ptr] + _PERM + [_c_i64, _c_ptr] + _WS),
+    "moe_combine": (_c_int, [_c_ptr] + _PERM + [_c_ptr, _c_i64, _c_ptr] + _WS),
+    "moe_combine_bwd": (_c_int, [_c_ptr, _c_ptr] + _PERM + [_c_ptr, _c_i64, _c_ptr, _c_ptr] + _WS),
+    "avr_fp8_scales_bytes": (_c_size, [_c_i64, _c_i64]),
+    "fp8_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "fp8_quant": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_fp8] + _WS),
+    "fp8_quant_t": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_fp8] + _WS),
+    "fp8_quant_weight": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_fp8, _c_fp8] + _WS),
+    "fp8_gemm": (_c_int, [_c_fp8, _c_fp8, _c_ptr, _c_int] + _WS),
+    "fp8_linear_fwd": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_fp8, _c_ptr, _c_int] + _WS),
+    "fp8_linear_dgrad": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_fp8, _c_ptr, _c_int] + _WS),
+    "fp8_linear_wgrad": (_c_int, [_c_ptr, _c_int, _c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_int] + _WS),
+    "fp8_moe_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int]),
+    "fp8_moe_quant_weights": (_c_int, [_c_ptr, _c_int, _c_int, _c_i64, _c_i64, _c_fp8, _c_fp8] + _WS),
+    "fp8_moe_dispatch": (_c_int, [_c_ptr] + _PERM + [_c_fp8] + _WS),
+    "fp8_moe_gemm": (_c_int, [_c_fp8, _c_ptr, _c_int, _c_fp8, _c_ptr, _c_int] + _WS),
+    "fp8_moe_linear_fwd": (_c_int, [_c_ptr, _c_int, _c_i64, _c_ptr, _c_int, _c_i64, _c_i64, _c_fp8, _c_ptr, _c_int]
+                           + _WS),
+    "fp8_moe_linear_dgrad": (_c_int, [_c_ptr, _c_int, _c_i64, _c_ptr, _c_int, _c_i64, _c_i64, _c_fp8, _c_ptr, _c_int]
+                             + _WS),
+    "fp8_moe_linear_wgrad": (_c_int, [_c_ptr, _c_int, _c_ptr, _c_int, _c_i64, _c_ptr, _c_int, _c_i64, _c_i64, _c_ptr,
+                                      _c_int] + _WS),
+})
 
 
 def library_path():
@@ -440,3 +478,282 @@ def averis_split_quant_noalloc(X, rm, seed, offset, grad, mu, mu_q, xr_q, xr_deb
                                              int(grad), _ptr(mu), _s(mu_q), _s(xr_q), _ptr(xr_debug),
                                              _ptr(device_status), _stream(stream)),
            "averis_split_quant_noalloc")
+
+
+# ---------------------------------------------------------------------------
+# routing and 8-bit calls: the tensors are contiguous and on the current
+# device, else AverisError (invalid argument) before any launch
+# ---------------------------------------------------------------------------
+def _call(name, stream, ws, *args, tensors=()):
+    """The entry point with ws, its size and the stream appended."""
+    dev = torch.cuda.current_device()
+    for t in tensors + (ws,):
+        if t is not None and not (t.is_contiguous() and t.get_device() == dev):
+            raise AverisError(AVR_ERR_INVALID_ARG, f"{name}: every tensor must be contiguous and on device {dev}")
+    st = getattr(_LIB or load(), name)(*args, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                       (stream or torch.cuda.current_stream()).cuda_stream)
+    if st != AVR_OK:
+        raise AverisError(st, name)
+
+
+def _shape(name, t, shape, dtype):
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise AverisError(AVR_ERR_INVALID_ARG,
+                          f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _route_workspace(n, device, stream):
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    averis_workspace_init(ws, stream)
+    return ws
+
+
+def moe_route_workspace_size(T, k, E):
+    return int(load().moe_route_workspace_size(T, k, E))
+
+
+def moe_route_workspace(T, k, E, device="cuda", stream=None):
+    """A workspace for the routing calls of T tokens, k slots, E experts."""
+    return _route_workspace(_positive(moe_route_workspace_size(T, k, E), "moe_route_workspace"), device, stream)
+
+
+def _positive(n, where):
+    if n == 0:
+        raise AverisError(AVR_ERR_UNSUPPORTED_SHAPE, where)
+    return n
+
+
+def moe_max_rows(T, k, E):
+    """Rows of an experts' buffer that any routing of T tokens to k of E experts fits in."""
+    return (T * k + 127 * min(E, T * k)) // 128 * 128
+
+
+def moe_route(logits, norm, ids, weights, ws, stream=None):
+    T, E = logits.shape
+    k = ids.shape[1]
+    _shape("moe_route", ids, (T, k), torch.int32)
+    _shape("moe_route", weights, (T, k), torch.float32)
+    _call("moe_route", stream, ws, logits.data_ptr(), _dtype(logits), T, E, k, int(norm), ids.data_ptr(),
+          weights.data_ptr(), tensors=(logits, ids, weights))
+
+
+def moe_route_bwd(logits, norm, ids, weights, dweights, dlogits, ws, stream=None):
+    """logits may be None when norm is true."""
+    T, E = dlogits.shape
+    k = ids.shape[1]
+    if logits is not None:
+        _shape("moe_route_bwd", logits, (T, E), dlogits.dtype)
+    _shape("moe_route_bwd", ids, (T, k), torch.int32)
+    _shape("moe_route_bwd", weights, (T, k), torch.float32)
+    _shape("moe_route_bwd", dweights, (T, k), torch.float32)
+    _call("moe_route_bwd", stream, ws, None if logits is None else logits.data_ptr(), _dtype(dlogits), T, E, k,
+          int(norm), ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(),
+          tensors=(logits, ids, weights, dweights, dlogits))
+
+
+def moe_sort(ids, l_cap, counts, row, ws, stream=None):
+    T, k = ids.shape
+    _shape("moe_sort", ids, (T, k), torch.int32)
+    _shape("moe_sort", row, (T, k), torch.int32)
+    _shape("moe_sort", counts, (counts.numel(),), torch.int32)
+    _call("moe_sort", stream, ws, ids.data_ptr(), T, k, counts.numel(), l_cap, counts.data_ptr(), row.data_ptr(),
+          tensors=(ids, counts, row))
+
+
+def _permute_shapes(name, tokens, row, *bufs):
+    T, H = tokens.shape
+    k, l_cap = row.shape[1], bufs[0].shape[0]
+    _shape(name, row, (T, k), torch.int32)
+    for b in bufs:
+        _shape(name, b, (l_cap, H), tokens.dtype)
+    return T, k, H, l_cap
+
+
+def moe_dispatch(X, row, Xp, ws, stream=None):
+    T, k, H, l_cap = _permute_shapes("moe_dispatch", X, row, Xp)
+    _call("moe_dispatch", stream, ws, X.data_ptr(), _dtype(X), T, k, H, row.data_ptr(), l_cap, Xp.data_ptr(),
+          tensors=(X, row, Xp))
+
+
+def moe_dispatch_bwd(dXp, row, dX, ws, stream=None):
+    T, k, H, l_cap = _permute_shapes("moe_dispatch_bwd", dX, row, dXp)
+    _call("moe_dispatch_bwd", stream, ws, dXp.data_ptr(), _dtype(dX), T, k, H, row.data_ptr(), l_cap, dX.data_ptr(),
+          tensors=(dXp, row, dX))
+
+
+def moe_combine(Yp, row, weights, Y, ws, stream=None):
+    T, k, H, l_cap = _permute_shapes("moe_combine", Y, row, Yp)
+    _shape("moe_combine", weights, (T, k), torch.float32)
+    _call("moe_combine", stream, ws, Yp.data_ptr(), _dtype(Y), T, k, H, row.data_ptr(), weights.data_ptr(), l_cap,
+          Y.data_ptr(), tensors=(Yp, row, weights, Y))
+
+
+def moe_combine_bwd(dY, Yp, row, weights, dYp, dweights, ws, stream=None):
+    T, k, H, l_cap = _permute_shapes("moe_combine_bwd", dY, row, Yp, dYp)
+    _shape("moe_combine_bwd", weights, (T, k), torch.float32)
+    _shape("moe_combine_bwd", dweights, (T, k), torch.float32)
+    _call("moe_combine_bwd", stream, ws, dY.data_ptr(), Yp.data_ptr(), _dtype(dY), T, k, H, row.data_ptr(),
+          weights.data_ptr(), l_cap, dYp.data_ptr(), dweights.data_ptr(),
+          tensors=(dY, Yp, row, weights, dYp, dweights))
+
+
+class FP8Tensor:
+    """Device storage of an 8-bit tensor [rows, K]: E4M3 codes and one scale
+    byte per row and 128 elements of K in the atom layout of averis.h."""
+
+    def __init__(self, rows, K, device="cuda"):
+        n = avr_fp8_scales_bytes(rows, K)
+        if rows > 0:
+            _positive(n, "FP8Tensor")
+        self.rows, self.K = int(rows), int(K)
+        self.codes = torch.empty((self.rows, self.K), dtype=torch.uint8, device=device)
+        self.scales = torch.empty(n, dtype=torch.uint8, device=device)
+
+    @classmethod
+    def of(cls, codes, scales):
+        """The tensor held by codes [rows, K] and scales (uint8, not copied)."""
+        t = cls.__new__(cls)
+        t.rows, t.K = codes.shape
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 \
+                or scales.numel() != avr_fp8_scales_bytes(t.rows, t.K):
+            raise AverisError(AVR_ERR_INVALID_ARG, "FP8Tensor.of")
+        t.codes, t.scales = codes, scales
+        return t
+
+    def struct(self):
+        return avr_fp8(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.K)
+
+
+def _q(t):
+    return (None, ()) if t is None else (ctypes.byref(t.struct()), (t.codes, t.scales))
+
+
+def avr_fp8_scales_bytes(rows, K):
+    return int(load().avr_fp8_scales_bytes(rows, K))
+
+
+def fp8_workspace_size(l, m, n):
+    return int(load().fp8_workspace_size(l, m, n))
+
+
+def fp8_workspace(l, m, n, device="cuda", stream=None):
+    """A workspace for the 8-bit calls of l tokens, m input and n output features."""
+    return _route_workspace(_positive(fp8_workspace_size(l, m, n), "fp8_workspace"), device, stream)
+
+
+def fp8_quant(X, out, ws, stream=None):
+    rows, K = X.shape
+    q, t = _q(out)
+    _call("fp8_quant", stream, ws, X.data_ptr(), _dtype(X), rows, K, q, tensors=(X,) + t)
+
+
+def fp8_quant_t(X, out, ws, stream=None):
+    """out: FP8Tensor(K, l rounded up to 128)."""
+    l, K = X.shape
+    q, t = _q(out)
+    _call("fp8_quant_t", stream, ws, X.data_ptr(), _dtype(X), l, K, q, tensors=(X,) + t)
+
+
+def fp8_quant_weight(W, w_fwd, w_dgrad, ws, stream=None):
+    """w_dgrad may be None."""
+    m, n = W.shape
+    (f, tf), (d, td) = _q(w_fwd), _q(w_dgrad)
+    _call("fp8_quant_weight", stream, ws, W.data_ptr(), _dtype(W), m, n, f, d, tensors=(W,) + tf + td)
+
+
+def fp8_gemm(a, b, Y, ws, stream=None):
+    (qa, ta), (qb, tb) = _q(a), _q(b)
+    _shape("fp8_gemm", Y, (a.rows, b.rows), Y.dtype)
+    _call("fp8_gemm", stream, ws, qa, qb, Y.data_ptr(), _dtype(Y), tensors=(Y,) + ta + tb)
+
+
+def fp8_linear_fwd(X, w_fwd, Y, ws, stream=None):
+    l, m = X.shape
+    q, t = _q(w_fwd)
+    _shape("fp8_linear_fwd", Y, (l, w_fwd.rows), Y.dtype)
+    _call("fp8_linear_fwd", stream, ws, X.data_ptr(), _dtype(X), l, m, w_fwd.rows, q, Y.data_ptr(), _dtype(Y),
+          tensors=(X, Y) + t)
+
+
+def fp8_linear_dgrad(D, w_dgrad, dX, ws, stream=None):
+    l, n = D.shape
+    q, t = _q(w_dgrad)
+    _shape("fp8_linear_dgrad", dX, (l, w_dgrad.rows), dX.dtype)
+    _call("fp8_linear_dgrad", stream, ws, D.data_ptr(), _dtype(D), l, w_dgrad.rows, n, q, dX.data_ptr(), _dtype(dX),
+          tensors=(D, dX) + t)
+
+
+def fp8_linear_wgrad(X, D, dW, ws, stream=None):
+    l, m = X.shape
+    n = D.shape[1]
+    _shape("fp8_linear_wgrad", D, (l, n), D.dtype)
+    _shape("fp8_linear_wgrad", dW, (m, n), dW.dtype)
+    _call("fp8_linear_wgrad", stream, ws, X.data_ptr(), _dtype(X), D.data_ptr(), _dtype(D), l, m, n, dW.data_ptr(),
+          _dtype(dW), tensors=(X, D, dW))
+
+
+def fp8_moe_workspace_size(l_cap, m, n, E):
+    return int(load().fp8_moe_workspace_size(l_cap, m, n, E))
+
+
+def fp8_moe_workspace(l_cap, m, n, E, slots=0, device="cuda", stream=None):
+    """A workspace for the experts' 8-bit calls, and for the routing calls of
+    up to `slots` = T k slots."""
+    need = _positive(fp8_moe_workspace_size(l_cap, m, n, E), "fp8_moe_workspace")
+    return _route_workspace(max(need, moe_route_workspace_size(slots, 1, E)), device, stream)
+
+
+def fp8_moe_quant_weights(W, w_fwd, w_dgrad, ws, stream=None):
+    """w_dgrad may be None."""
+    E, m, n = W.shape
+    (f, tf), (d, td) = _q(w_fwd), _q(w_dgrad)
+    _call("fp8_moe_quant_weights", stream, ws, W.data_ptr(), _dtype(W), E, m, n, f, d, tensors=(W,) + tf + td)
+
+
+def fp8_moe_dispatch(X, row, xq, ws, stream=None):
+    T, K = X.shape
+    k = row.shape[1]
+    q, t = _q(xq)
+    _shape("fp8_moe_dispatch", row, (T, k), torch.int32)
+    _call("fp8_moe_dispatch", stream, ws, X.data_ptr(), _dtype(X), T, k, K, row.data_ptr(), q, tensors=(X, row) + t)
+
+
+def fp8_moe_gemm(xq, counts, w, Y, ws, stream=None):
+    (qx, tx), (qw, tw) = _q(xq), _q(w)
+    E = counts.numel()
+    _shape("fp8_moe_gemm", counts, (E,), torch.int32)
+    _shape("fp8_moe_gemm", Y, (xq.rows, w.rows // max(E, 1)), Y.dtype)
+    _call("fp8_moe_gemm", stream, ws, qx, counts.data_ptr(), E, qw, Y.data_ptr(), _dtype(Y),
+          tensors=(counts, Y) + tx + tw)
+
+
+def _moe_shapes(name, X, counts, w, Y):
+    l_cap, E = X.shape[0], counts.numel()
+    _shape(name, counts, (E,), torch.int32)
+    N = w.rows // max(E, 1)
+    _shape(name, Y, (l_cap, N), Y.dtype)
+    return l_cap, E, X.shape[1], N
+
+
+def fp8_moe_linear_fwd(X, counts, w_fwd, Y, ws, stream=None):
+    l_cap, E, m, n = _moe_shapes("fp8_moe_linear_fwd", X, counts, w_fwd, Y)
+    q, t = _q(w_fwd)
+    _call("fp8_moe_linear_fwd", stream, ws, X.data_ptr(), _dtype(X), l_cap, counts.data_ptr(), E, m, n, q,
+          Y.data_ptr(), _dtype(Y), tensors=(X, counts, Y) + t)
+
+
+def fp8_moe_linear_dgrad(D, counts, w_dgrad, dX, ws, stream=None):
+    l_cap, E, n, m = _moe_shapes("fp8_moe_linear_dgrad", D, counts, w_dgrad, dX)
+    q, t = _q(w_dgrad)
+    _call("fp8_moe_linear_dgrad", stream, ws, D.data_ptr(), _dtype(D), l_cap, counts.data_ptr(), E, m, n, q,
+          dX.data_ptr(), _dtype(dX), tensors=(D, counts, dX) + t)
+
+
+def fp8_moe_linear_wgrad(X, D, counts, dW, ws, stream=None):
+    l_cap, m = X.shape
+    n, E = D.shape[1], counts.numel()
+    _shape("fp8_moe_linear_wgrad", D, (l_cap, n), D.dtype)
+    _shape("fp8_moe_linear_wgrad", counts, (E,), torch.int32)
+    _shape("fp8_moe_linear_wgrad", dW, (E, m, n), dW.dtype)
+    _call("fp8_moe_linear_wgrad", stream, ws, X.data_ptr(), _dtype(X), D.data_ptr(), _dtype(D), l_cap,
+          counts.data_ptr(), E, m, n, dW.data_ptr(), _dtype(dW), tensors=(X, D, counts, dW))

@@ -1,0 +1,449 @@
+// Quantizers of the 8-bit linear layer: E4M3 codes with a power-of-two scale
+// per block of 128 (the rule is in include/averis.h), written in the layouts
+// the block-scaled product reads.
+//
+// Every element is read once and its byte written once: 3 bytes of memory
+// traffic an element from bf16, 5 from fp32, and a few instructions; the
+// kernels are bound by memory.  The largest magnitude of a block is taken on
+// the bit patterns (an integer maximum orders them, and unlike a float maximum
+// keeps a NaN), so the exponent and the non-finite check fall out of it.
+#include <cuda_bf16.h>
+
+#include "device.cuh"
+#include "route.h"
+
+namespace avr {
+
+namespace {
+
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// scale byte e + 127 of a block whose largest magnitude has these bits: 448 =
+// 1.75 * 2^8, so e = exponent - 8, one more when the significand passes 1.75
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+  const int b = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return static_cast<uint32_t>(b > 0 ? b : 0);
+}
+// 2^-e, exact: the byte is at most 247
+__device__ __forceinline__ float inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// two values -> two E4M3 codes, nearest even (lo in the low byte)
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+// 16 bytes of input: N values, as fp32 and as the largest magnitude's bits
+template <bool kBf16>
+struct In {
+  static constexpr int kN = kBf16 ? 8 : 4;
+};
+template <bool kBf16>
+__device__ __forceinline__ float value_of(const uint4& q, int i) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if (!kBf16) return __uint_as_float(w[i]);
+  return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t amax_bits(const uint4& q) {
+  if (kBf16) {
+    const uint32_t m = __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
+                                __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
+    return max(m & 0xFFFF0000u, m << 16);
+  }
+  return max(max(q.x & 0x7FFFFFFFu, q.y & 0x7FFFFFFFu), max(q.z & 0x7FFFFFFFu, q.w & 0x7FFFFFFFu));
+}
+
+// byte of (row r, block c) in the atom layout
+__device__ __forceinline__ int64_t scale_at(int64_t r, int64_t c, int64_t atoms) {
+  return ((r >> 7) * atoms + (c >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (c & 3);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// segment table of the experts' buffer (one CTA)
+// ---------------------------------------------------------------------------
+constexpr int kTableThreads = 1024;
+
+__global__ void __launch_bounds__(kTableThreads) fp8_table_kernel(const int32_t* counts, int E, int64_t l_cap,
+                                                                  const Fp8Table t, uint32_t* status) {
+  __shared__ int32_t s_rows[kMaxExperts], s_blk[kMaxExperts], s_tile[kMaxExperts];   // rows; ends in blocks, tiles
+  __shared__ uint64_t s_warp[32];
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t n = tid < E ? __ldg(counts + tid) : 0;
+  const bool bad = n < 0 || n > l_cap;
+  const bool any_bad = __syncthreads_or(bad) != 0;
+  // blocks in the low 35 bits of a word (1024 counts of at most 2^24 blocks),
+  // tiles above them: when the segments fit there are at most 2^24 tiles
+  constexpr int kShift = 35;
+  constexpr uint64_t kLow = (1ull << kShift) - 1;
+  const uint64_t blk = bad ? 0 : (static_cast<uint64_t>(n) + 127) / 128;
+  uint64_t x = blk | (((blk + 1) / 2) << kShift);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    uint64_t y = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t z = __shfl_up_sync(kFull, y, o);
+      if (lane >= o) y += z;
+    }
+    s_warp[lane] = y;
+  }
+  __syncthreads();
+  if (warp > 0) x += s_warp[warp - 1];
+  const uint64_t all = s_warp[31];
+  const int64_t n_blocks = l_cap / 128;
+  const bool fits = !any_bad && static_cast<int64_t>(all & kLow) <= n_blocks;
+  const int32_t blocks = fits ? static_cast<int32_t>(all & kLow) : 0;
+  const int32_t tiles = fits ? static_cast<int32_t>(all >> kShift) : 0;
+  if (tid < E && fits) {
+    s_rows[tid] = n;
+    s_blk[tid] = static_cast<int32_t>(x & kLow);
+    s_tile[tid] = static_cast<int32_t>(x >> kShift);
+    t.seg[tid] = Fp8Seg{static_cast<int32_t>(128 * ((x & kLow) - blk)), n};
+  }
+  if (tid == 0) {
+    t.totals[0] = tiles;
+    t.totals[1] = fits ? 1 : 0;
+    if (!fits) raise_status(status, AVR_ERR_INVALID_ARG);
+  }
+  __syncthreads();
+  // the first expert whose end lies past i
+  auto find = [&](const int32_t* end, int32_t i) {
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (end[mid] > i)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    return lo;
+  };
+  for (int32_t b = tid; b < n_blocks; b += kTableThreads) t.block_expert[b] = b < blocks ? find(s_blk, b) : -1;
+  for (int32_t i = tid; i < tiles; i += kTableThreads) {
+    const int e = find(s_tile, i);
+    const int32_t first_tile = e > 0 ? s_tile[e - 1] : 0, first_blk = e > 0 ? s_blk[e - 1] : 0;
+    const int32_t off = 256 * (i - first_tile);
+    t.tiles[i] = Fp8Tile{128 * first_blk + off, e, min(256, s_rows[e] - off), 0};
+  }
+}
+
+cudaError_t launch_fp8_table(const int32_t* counts, int E, int64_t l_cap, const Fp8Table& t, uint32_t* status,
+                             cudaStream_t s) {
+  return launch_ex(fp8_table_kernel, dim3(1), dim3(kTableThreads), 0, s, true, counts, E, l_cap, t, status);
+}
+
+// ---------------------------------------------------------------------------
+// along K: a warp takes kRows rows x 512 columns, 16 columns a lane, so that
+// eight lanes share a block and the warp's four scale bytes are one word of an
+// atom
+// ---------------------------------------------------------------------------
+constexpr int kQThreads = 256;
+constexpr int kQWarps = kQThreads / 32;
+
+template <bool kBf16>
+__device__ __forceinline__ void quant_strip(const uint4 (&q)[16 / In<kBf16>::kN], uint4* codes, uint32_t* word,
+                                            bool* bad) {
+  constexpr int N = In<kBf16>::kN, Q = 16 / N;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) m = max(m, amax_bits<kBf16>(q[i]));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+  *bad |= m >= kInfBits;
+  const uint32_t byte = scale_byte(m);
+  const float inv = inv_scale(byte);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) f[c] = value_of<kBf16>(q[(4 * i + c) / N], (4 * i + c) % N) * inv;
+    w[i] = e4m3x4(f[0], f[1], f[2], f[3]);
+  }
+  *codes = make_uint4(w[0], w[1], w[2], w[3]);
+  const int lane = threadIdx.x & 31;
+  *word = __reduce_or_sync(kFull, (lane & 7) == 0 ? byte << (lane & 24) : 0u);
+}
+
+enum class Rows { kAll, kGrouped, kDispatch };
+
+template <bool kBf16, Rows kMode, int kRows>
+__global__ void __launch_bounds__(kQThreads) fp8_quant_kernel(const Fp8QuantArgs a, const Fp8Table t, int64_t rows_pad,
+                                                              int strips) {
+  constexpr int N = In<kBf16>::kN, Q = 16 / N;
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  if (kMode == Rows::kGrouped && __ldcg(t.totals + 1) == 0) return;
+  const int lane = threadIdx.x & 31;
+  const uint4* X = static_cast<const uint4*>(a.X);
+  const int64_t V = a.K / N;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kQWarps;
+  const int64_t tasks = (rows_pad / kRows) * strips;
+  bool bad = false;
+  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kQWarps + (threadIdx.x >> 5); task < tasks; task += warps) {
+    const int strip = static_cast<int>(task % strips);
+    const int64_t r0 = task / strips * kRows;
+    const int64_t col = static_cast<int64_t>(strip) * 512 + 16 * lane;
+    int64_t end = a.rows;
+    if (kMode == Rows::kGrouped) {        // a task lies in one 128-row block, so in one segment
+      const int e = __ldcg(t.block_expert + r0 / 128);
+      if (e < 0) break;                   // past the last segment, and so is all that follows
+      const int2 sg = __ldcg(reinterpret_cast<const int2*>(t.seg + e));
+      end = static_cast<int64_t>(sg.x) + sg.y;
+    }
+    uint4 q[kRows][Q];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+      for (int u = 0; u < Q; ++u)
+        q[i][u] = (r0 + i < end && col < a.K) ? __ldg(X + (r0 + i) * V + col / N + u) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t r = r0 + i;
+      if (kMode != Rows::kAll && r >= end) break;      // the whole warp
+      uint4 codes;
+      uint32_t word;
+      quant_strip<kBf16>(q[i], &codes, &word, &bad);
+      auto put = [&](int64_t dst) {
+        if (col < a.K) *reinterpret_cast<uint4*>(a.codes + dst * a.K + col) = codes;
+        if (lane == 0) *reinterpret_cast<uint32_t*>(a.scales + scale_at(dst, 4 * strip, strips)) = word;
+      };
+      if (kMode == Rows::kDispatch) {
+        for (int j = 0; j < a.k; ++j) {
+          const int32_t dst = __ldg(a.row + r * a.k + j);
+          if (dst >= a.l_cap) raise_status(a.status, AVR_ERR_INVALID_ARG);
+          if (dst >= 0 && dst < a.l_cap) put(dst);
+        }
+      } else if (r < end) {
+        put(r);
+      } else if (lane == 0) {             // rows up to the next multiple of 128: zero scales
+        *reinterpret_cast<uint32_t*>(a.scales + scale_at(r, 4 * strip, strips)) = 0u;
+      }
+    }
+  }
+  if (bad) raise_status(a.status, AVR_ERR_NONFINITE);
+}
+
+template <bool kBf16, Rows kMode, int kRows>
+static cudaError_t quant_t(const Fp8QuantArgs& a, int64_t rows_pad, cudaStream_t s) {
+  auto kern = fp8_quant_kernel<kBf16, kMode, kRows>;
+  const int strips = static_cast<int>((a.K + 511) / 512);
+  const int64_t need = (rows_pad / kRows * strips + kQWarps - 1) / kQWarps;
+  const int64_t most = static_cast<int64_t>(sm_count()) *
+                       blocks_per_sm(reinterpret_cast<const void*>(kern), kQThreads, 0) * 4;
+  const Fp8Table t = a.table ? *a.table : Fp8Table{};
+  return launch_ex(kern, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(kQThreads), 0, s, true, a, t,
+                   rows_pad, strips);
+}
+
+cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, cudaStream_t s) {
+  const int64_t pad = blocks128(a.rows) * 128;
+  if (a.row != nullptr)
+    return a.xt == AVR_BF16 ? quant_t<true, Rows::kDispatch, 1>(a, a.rows, s)
+                            : quant_t<false, Rows::kDispatch, 1>(a, a.rows, s);
+  if (a.table != nullptr)
+    return a.xt == AVR_BF16 ? quant_t<true, Rows::kGrouped, 4>(a, pad, s) : quant_t<false, Rows::kGrouped, 4>(a, pad, s);
+  return a.xt == AVR_BF16 ? quant_t<true, Rows::kAll, 4>(a, pad, s) : quant_t<false, Rows::kAll, 4>(a, pad, s);
+}
+
+// ---------------------------------------------------------------------------
+// along the tokens: a CTA takes 128 tokens x 8 vectors of features (64 bf16,
+// 32 fp32).  A thread holds four consecutive tokens of one vector, so its
+// codes of a feature are one word of the transposed tile; the tile goes
+// through shared memory (rows of 33 words) and out as full 128-byte lines.
+// ---------------------------------------------------------------------------
+template <bool kBf16>
+__global__ void __launch_bounds__(kQThreads) fp8_quant_tokens_kernel(const Fp8QuantArgs a, const Fp8Table t,
+                                                                     int64_t L, int64_t atoms, unsigned ftiles) {
+  constexpr int N = In<kBf16>::kN, F = 8 * N;
+  __shared__ uint32_t s_max[kQWarps][F];
+  __shared__ uint32_t s_tile[F][33];
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t f0 = blockIdx.x % ftiles * F, c = blockIdx.x / ftiles;   // feature tiles fastest: they share rows
+  int64_t end = a.rows;
+  if (a.table != nullptr) {
+    if (__ldcg(t.totals + 1) == 0) return;
+    const int e = __ldcg(t.block_expert + c);
+    if (e < 0) return;
+    const int2 sg = __ldcg(reinterpret_cast<const int2*>(t.seg + e));
+    end = static_cast<int64_t>(sg.x) + sg.y;
+  }
+  const int v = tid & 7, g = tid >> 3;               // vector, group of four tokens
+  const uint4* X = static_cast<const uint4*>(a.X);
+  const int64_t V = a.K / N, vec = f0 / N + v;
+  uint4 q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = c * 128 + 4 * g + i;
+    q[i] = (r < end && vec < V) ? __ldg(X + r * V + vec) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  uint32_t m[N];
+#pragma unroll
+  for (int f = 0; f < N; ++f) {
+    m[f] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[f] = max(m[f], __float_as_uint(value_of<kBf16>(q[i], f)) & 0x7FFFFFFFu);
+    m[f] = max(m[f], __shfl_xor_sync(kFull, m[f], 8));
+    m[f] = max(m[f], __shfl_xor_sync(kFull, m[f], 16));
+    if (lane < 8) s_max[warp][N * v + f] = m[f];
+  }
+  __syncthreads();
+  bool bad = false;
+  if (tid < F) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int w = 0; w < kQWarps; ++w) top = max(top, s_max[w][tid]);
+    bad = top >= kInfBits;
+    const uint32_t byte = scale_byte(top);
+    s_max[0][tid] = byte;                            // this thread alone reads and writes the column here
+    const int64_t j = f0 + tid, at = scale_at(j, c, atoms);
+    a.scales[at] = static_cast<uint8_t>(j < a.K ? byte : 0u);
+    if (c == L / 128 - 1)                            // the atom's blocks past the last
+      for (int64_t z = c + 1; z < 4 * atoms; ++z) a.scales[scale_at(j, z, atoms)] = 0;
+  }
+  if (bad) raise_status(a.status, AVR_ERR_NONFINITE);
+  __syncthreads();
+#pragma unroll
+  for (int f = 0; f < N; ++f) {
+    const float inv = inv_scale(s_max[0][N * v + f]);
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = value_of<kBf16>(q[i], f) * inv;
+    s_tile[N * v + f][g] = e4m3x4(x[0], x[1], x[2], x[3]);
+  }
+  __syncthreads();
+  for (int f = warp; f < F; f += kQWarps)
+    if (f0 + f < a.K) *reinterpret_cast<uint32_t*>(a.codes + (f0 + f) * L + c * 128 + 4 * lane) = s_tile[f][lane];
+}
+
+cudaError_t launch_fp8_quant_t(const Fp8QuantArgs& a, cudaStream_t s) {
+  const int64_t L = blocks128(a.rows) * 128;
+  const int F = a.xt == AVR_BF16 ? 64 : 32;
+  const int64_t ftiles = blocks128(a.K) * 128 / F, grid = ftiles * (L / 128);
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const Fp8Table t = a.table ? *a.table : Fp8Table{};
+  auto kern = a.xt == AVR_BF16 ? fp8_quant_tokens_kernel<true> : fp8_quant_tokens_kernel<false>;
+  return launch_ex(kern, dim3(static_cast<unsigned>(grid)), dim3(kQThreads), 0, s, true, a, t, L, atoms128(L),
+                   static_cast<unsigned>(ftiles));
+}
+
+// ---------------------------------------------------------------------------
+// weights: a CTA takes one 128 x 128 block and writes it both ways round, the
+// transposed codes through shared memory
+// ---------------------------------------------------------------------------
+template <bool kBf16>
+__global__ void __launch_bounds__(kQThreads)
+    fp8_quant_weight_kernel(const void* W, int64_t m, int64_t n, uint8_t* fwd_codes, uint8_t* fwd_scales,
+                            uint8_t* dg_codes, uint8_t* dg_scales, int64_t atoms_m, int64_t atoms_n, uint32_t* status) {
+  constexpr int N = In<kBf16>::kN, kCols = 128 / N;    // vectors of a row: 16 (bf16) or 32
+  constexpr int kGroups = kQThreads / kCols;           // row groups: 16 or 8
+  constexpr int R = 128 / kGroups;                     // consecutive rows of a thread: 8 or 16
+  __shared__ uint32_t s_max[kQWarps];
+  __shared__ uint32_t s_tile[128][33];
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t bns = (n + 127) / 128, bms = (m + 127) / 128;
+  const int64_t bn = blockIdx.x % bns, bm = blockIdx.x / bns % bms, e = blockIdx.x / bns / bms;
+  const int v = tid % kCols, g = tid / kCols;
+  const uint4* X = static_cast<const uint4*>(W) + e * m * (n / N);
+  const int64_t V = n / N, vec = bn * kCols + v;
+  uint4 q[R];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t r = bm * 128 + R * g + i;
+    q[i] = (r < m && vec < V) ? __ldg(X + r * V + vec) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) top = max(top, amax_bits<kBf16>(q[i]));
+  top = __reduce_max_sync(kFull, top);
+  if (lane == 0) s_max[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kQWarps; ++w) top = max(top, s_max[w]);
+  if (top >= kInfBits && tid == 0) raise_status(status, AVR_ERR_NONFINITE);
+  const uint32_t byte = scale_byte(top);
+  const float inv = inv_scale(byte);
+  // rows of this thread, N codes each
+#pragma unroll
+  for (int i4 = 0; i4 < R / 4; ++i4) {
+    uint32_t w[4][N / 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int b = 0; b < N / 4; ++b) {
+        float f[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) f[x] = value_of<kBf16>(q[4 * i4 + i], 4 * b + x) * inv;
+        w[i][b] = e4m3x4(f[0], f[1], f[2], f[3]);
+      }
+      const int64_t r = bm * 128 + R * g + 4 * i4 + i;
+      if (dg_codes != nullptr && r < m && vec < V) {
+        uint8_t* dst = dg_codes + (e * m + r) * n + vec * N;
+        if (N == 8)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(w[i][0], w[i][N / 4 - 1]);
+        else
+          *reinterpret_cast<uint32_t*>(dst) = w[i][0];
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < N / 4; ++b) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {                    // feature 4 b + x: four rows' codes as one word
+        const uint32_t lo = __byte_perm(w[0][b], w[1][b], x | ((x + 4) << 4));
+        const uint32_t hi = __byte_perm(w[2][b], w[3][b], x | ((x + 4) << 4));
+        s_tile[N * v + 4 * b + x][(R * g) / 4 + i4] = (lo & 0xFFFFu) | (hi << 16);
+      }
+    }
+  }
+  __syncthreads();
+  // w_fwd: feature rows of m codes (m % 16 == 0, so a word is wholly inside or outside)
+  for (int f = warp; f < 128; f += kQWarps)
+    if (bn * 128 + f < n && bm * 128 + 4 * lane < m)
+      *reinterpret_cast<uint32_t*>(fwd_codes + (e * n + bn * 128 + f) * m + bm * 128 + 4 * lane) = s_tile[f][lane];
+  if (tid < 128) {
+    // experts are stacked by whole 128-row groups (E > 1 needs m and n in multiples of 128)
+    const int64_t j = e * n + bn * 128 + tid;
+    fwd_scales[scale_at(j, bm, atoms_m)] = static_cast<uint8_t>(bn * 128 + tid < n ? byte : 0u);
+    if (bm == bms - 1)
+      for (int64_t z = bm + 1; z < 4 * atoms_m; ++z) fwd_scales[scale_at(j, z, atoms_m)] = 0;
+    if (dg_codes != nullptr) {
+      const int64_t i = e * m + bm * 128 + tid;
+      dg_scales[scale_at(i, bn, atoms_n)] = static_cast<uint8_t>(bm * 128 + tid < m ? byte : 0u);
+      if (bn == bns - 1)
+        for (int64_t z = bn + 1; z < 4 * atoms_n; ++z) dg_scales[scale_at(i, z, atoms_n)] = 0;
+    }
+  }
+}
+
+cudaError_t launch_fp8_quant_weight(const void* W, avr_dtype wt, int E, int64_t m, int64_t n, uint8_t* fwd_codes,
+                                    uint8_t* fwd_scales, uint8_t* dg_codes, uint8_t* dg_scales, uint32_t* status,
+                                    cudaStream_t s) {
+  const int64_t grid = blocks128(n) * blocks128(m) * E;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  auto kern = wt == AVR_BF16 ? fp8_quant_weight_kernel<true> : fp8_quant_weight_kernel<false>;
+  return launch_ex(kern, dim3(static_cast<unsigned>(grid)), dim3(kQThreads), 0, s, true, W, m, n, fwd_codes, fwd_scales,
+                   dg_codes, dg_scales, atoms128(m), atoms128(n), status);
+}
+
+}  // namespace avr

@@ -1,0 +1,585 @@
+// Routing of a mixture of experts: the router and its gradient, the sort of
+// tokens by expert, dispatch to the experts' buffer and combine with their
+// gradients (the formulas are in include/averis.h).
+//
+// None of these kernels has arithmetic to speak of: the router and the sort
+// of a decoding step are bound by launch latency, the rest by the bytes of
+// the buffers, each moved once.
+#include <cuda_bf16.h>
+
+#include "device.cuh"
+#include "route.h"
+
+namespace avr {
+
+namespace {
+
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  return kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+template <bool kBf16>
+__device__ __forceinline__ void store1(void* p, int64_t i, float v) {
+  if (kBf16)
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(p)[i] = v;
+}
+
+// 16 bytes of the tensors' type as fp32 values and back
+template <bool kBf16>
+struct Vec {
+  static constexpr int kN = kBf16 ? 8 : 4;
+};
+template <bool kBf16>
+__device__ __forceinline__ void unpack(const uint4& q, float (&f)[Vec<kBf16>::kN]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kBf16) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      f[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+template <bool kBf16>
+__device__ __forceinline__ uint4 pack(const float (&f)[Vec<kBf16>::kN]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kBf16) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    } else {
+      w[i] = __float_as_uint(f[i]);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// router: one warp per token, expert lane + 32 i in register i of a lane
+// ---------------------------------------------------------------------------
+constexpr int kRouteWarps = 4;
+
+// a key that orders as the value does, above 0 for every value but -inf (and
+// NaN); + 0.0f makes the two zeros one value
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  const uint32_t u = b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  return v > -INFINITY ? u : 0u;
+}
+
+// Each of the k steps takes the largest key of the warp and, among the lanes
+// that hold it, the lowest expert: two warp reductions.  A lane's own best is
+// kept as a key and a register index, searched again only after it was taken.
+template <bool kBf16, int NV>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const void* logits, int64_t T, int E, int k, int norm,
+                                                                 int32_t* ids, float* weights, uint32_t* status) {
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+  if (t >= T) return;
+  float v[NV];
+  uint32_t key[NV];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 32 * i;
+    v[i] = e < E ? load1<kBf16>(logits, t * E + e) : -INFINITY;
+    bad |= !(v[i] < INFINITY);
+    key[i] = order_key(v[i]);
+  }
+  if (__any_sync(kFull, bad)) {       // NaN or +inf: the token goes without experts
+    if (lane == 0) raise_status(status, AVR_ERR_NONFINITE);
+    if (lane < k) {
+      ids[t * k + lane] = -1;
+      weights[t * k + lane] = 0.0f;
+    }
+    return;
+  }
+  int my_id = -1;                     // lane j holds slot j
+  float my_v = -INFINITY, top = -INFINITY;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = key[0];
+    int at = 0;
+    float bv = v[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) {
+      if (key[i] > best) {            // strictly: the lower expert of equal ones
+        best = key[i];
+        at = i;
+        bv = v[i];
+      }
+    }
+    const uint32_t m = __reduce_max_sync(kFull, best);
+    if (m == 0u) break;               // only -inf left
+    const uint32_t e = __reduce_min_sync(kFull, best == m ? static_cast<uint32_t>(lane + 32 * at) : 0xFFFFFFFFu);
+    const float ev = __shfl_sync(kFull, bv, static_cast<int>(e & 31u));
+    if (j == 0) top = ev;
+    if (lane == j) {
+      my_id = static_cast<int>(e);
+      my_v = ev;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (static_cast<uint32_t>(lane + 32 * i) == e) key[i] = 0u;
+  }
+  const float mine = my_id >= 0 ? expf(my_v - top) : 0.0f;
+  float den = mine;
+  if (!norm) {
+    den = 0.0f;
+    if (top > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) den += expf(v[i] - top);
+    }
+  }
+  den = warp_sum(den);
+  if (lane < k) {
+    ids[t * k + lane] = my_id;
+    weights[t * k + lane] = my_id >= 0 ? mine / den : 0.0f;
+  }
+}
+
+// Gradient: lane j holds slot j; the chosen experts' terms are added into a
+// row of shared memory, so the logits' loop needs no search.
+template <bool kBf16, int NV>
+__global__ void __launch_bounds__(32 * kRouteWarps)
+    route_bwd_kernel(const void* logits, int64_t T, int E, int k, int norm, const int32_t* ids, const float* weights,
+                     const float* dweights, void* dlogits, uint32_t* status) {
+  __shared__ float s_row[kRouteWarps][32 * NV];
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int lane = threadIdx.x & 31;
+  float* row = s_row[threadIdx.x >> 5];
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+  if (t >= T) return;
+  int id = -1;
+  float w = 0.0f, dw = 0.0f;
+  if (lane < k) {
+    id = ids[t * k + lane];
+    if (id >= E) {
+      raise_status(status, AVR_ERR_INVALID_ARG);
+      id = -1;
+    }
+    if (id >= 0) {
+      w = weights[t * k + lane];
+      dw = dweights[t * k + lane];
+    }
+  }
+  const float s = warp_sum(w * dw);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) row[lane + 32 * i] = 0.0f;
+  __syncwarp();
+  // one slot after another: a row that names an expert twice adds in slot order
+  for (int j = 0; j < k; ++j) {
+    if (lane == j && id >= 0) row[id] += norm ? w * (dw - s) : w * dw;
+    __syncwarp();
+  }
+  if (norm) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lane + 32 * i < E) store1<kBf16>(dlogits, t * E + lane + 32 * i, row[lane + 32 * i]);
+    return;
+  }
+  float v[NV], top = -INFINITY, den = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 32 * i;
+    v[i] = e < E ? load1<kBf16>(logits, t * E + e) : -INFINITY;
+    top = fmaxf(top, v[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    v[i] = top > -INFINITY ? expf(v[i] - top) : 0.0f;
+    den += v[i];
+  }
+  den = warp_sum(den);
+  const float c = den > 0.0f ? s / den : 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (lane + 32 * i < E) store1<kBf16>(dlogits, t * E + lane + 32 * i, row[lane + 32 * i] - v[i] * c);
+}
+
+template <bool kBf16, int NV>
+static cudaError_t route_t(const void* logits, int64_t T, int E, int k, int norm, int32_t* ids, float* weights,
+                           const float* dweights, void* dlogits, uint32_t* status, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((T + kRouteWarps - 1) / kRouteWarps));
+  if (dlogits == nullptr)
+    return launch_ex(route_kernel<kBf16, NV>, grid, dim3(32 * kRouteWarps), 0, s, true, logits, T, E, k, norm, ids,
+                     weights, status);
+  return launch_ex(route_bwd_kernel<kBf16, NV>, grid, dim3(32 * kRouteWarps), 0, s, true, logits, T, E, k, norm, ids,
+                   weights, dweights, dlogits, status);
+}
+
+template <bool kBf16>
+static cudaError_t route_d(const void* logits, int64_t T, int E, int k, int norm, int32_t* ids, float* weights,
+                           const float* dweights, void* dlogits, uint32_t* status, cudaStream_t s) {
+#define AVR_ROUTE(NV) \
+  if (E <= 32 * NV) return route_t<kBf16, NV>(logits, T, E, k, norm, ids, weights, dweights, dlogits, status, s)
+  AVR_ROUTE(1);
+  AVR_ROUTE(2);
+  AVR_ROUTE(4);
+  AVR_ROUTE(8);
+  AVR_ROUTE(16);
+  AVR_ROUTE(32);
+#undef AVR_ROUTE
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_route(const void* logits, avr_dtype lt, int64_t T, int E, int k, int norm, int32_t* ids,
+                         float* weights, uint32_t* status, cudaStream_t s) {
+  return lt == AVR_BF16 ? route_d<true>(logits, T, E, k, norm, ids, weights, nullptr, nullptr, status, s)
+                        : route_d<false>(logits, T, E, k, norm, ids, weights, nullptr, nullptr, status, s);
+}
+
+cudaError_t launch_route_bwd(const void* logits, avr_dtype lt, int64_t T, int E, int k, int norm, const int32_t* ids,
+                             const float* weights, const float* dweights, void* dlogits, uint32_t* status,
+                             cudaStream_t s) {
+  int32_t* i = const_cast<int32_t*>(ids);
+  float* w = const_cast<float*>(weights);
+  return lt == AVR_BF16 ? route_d<true>(logits, T, E, k, norm, i, w, dweights, dlogits, status, s)
+                        : route_d<false>(logits, T, E, k, norm, i, w, dweights, dlogits, status, s);
+}
+
+// ---------------------------------------------------------------------------
+// sort by expert: a stable counting sort over G chunks of consecutive slots.
+// Kernel 1 counts each chunk's slots per expert; in kernel 2 every CTA adds up
+// the counts of the chunks before its own (a few tens of KB from L2), scans
+// the padded totals over the experts, and ranks its slots.  One chunk needs
+// only kernel 2, which then counts its slots itself.
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+
+int sort_chunks(int64_t slots) {
+  const int64_t g = (slots + kSortThreads - 1) / kSortThreads;
+  return static_cast<int>(g < 1 ? 1 : g > 128 ? 128 : g);
+}
+
+// expert of slot i, -1 for none (and for an id that no expert has)
+__device__ __forceinline__ int slot_expert(const int32_t* ids, int64_t i, int64_t end, int E, bool& bad) {
+  const int e = i < end ? __ldg(ids + i) : -1;
+  bad |= e >= E;
+  return e >= E ? -1 : e;
+}
+
+__device__ __forceinline__ void count_chunk(const int32_t* ids, int64_t lo, int64_t hi, int E, int32_t* s_cnt,
+                                            uint32_t* status) {
+  bool bad = false;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
+    const int e = slot_expert(ids, i, hi, E, bad);
+    if (e >= 0) atomicAdd(&s_cnt[e], 1);      // integers: any order gives the same counts
+  }
+  if (bad) raise_status(status, AVR_ERR_INVALID_ARG);
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int32_t* ids, int64_t slots, int64_t per,
+                                                                  int E, int32_t* hist, uint32_t* status) {
+  __shared__ int32_t s_cnt[kMaxExperts];
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  for (int e = threadIdx.x; e < E; e += kSortThreads) s_cnt[e] = 0;
+  __syncthreads();
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * per;
+  count_chunk(ids, lo, min64(slots, lo + per), E, s_cnt, status);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kSortThreads) hist[static_cast<int64_t>(blockIdx.x) * E + e] = s_cnt[e];
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+    sort_place_kernel(const int32_t* ids, int64_t slots, int64_t per, int E, int64_t l_cap, const int32_t* hist,
+                      int32_t* counts, int32_t* row, uint32_t* status) {
+  __shared__ int32_t s_total[kMaxExperts];    // all slots of an expert
+  __shared__ int32_t s_next[kMaxExperts];     // the buffer row of this chunk's next slot of an expert
+  __shared__ int64_t s_warp[kSortWarps];
+  extern __shared__ uint16_t s_in[];          // [kSortWarps][E] slots of a round, per warp
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int G = static_cast<int>(gridDim.x), g = static_cast<int>(blockIdx.x);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t lo = g * per, hi = min64(slots, lo + per);
+  for (int e = tid; e < E; e += kSortThreads) {
+    s_total[e] = 0;
+    s_next[e] = 0;
+  }
+  __syncthreads();
+  if (G == 1) {
+    count_chunk(ids, lo, hi, E, s_total, status);
+  } else {
+    // thread (slice, e): the chunks slice, slice + slices, ... of expert e
+    int ep = 32;
+    while (ep < E) ep <<= 1;
+    const int e = tid & (ep - 1), slices = kSortThreads / ep;
+    if (e < E) {
+      int32_t all = 0, before = 0;
+      for (int c = tid / ep; c < G; c += slices) {
+        const int32_t n = __ldcg(hist + static_cast<int64_t>(c) * E + e);
+        all += n;
+        before += c < g ? n : 0;
+      }
+      atomicAdd(&s_total[e], all);
+      atomicAdd(&s_next[e], before);
+    }
+  }
+  __syncthreads();
+  // exclusive scan of the padded totals over the experts (thread = expert)
+  const int64_t n = tid < E ? s_total[tid] : 0;
+  const int64_t pad = (n + 127) / 128 * 128;
+  int64_t x = pad;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t y = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t z = __shfl_up_sync(kFull, y, o);
+      if (lane >= o) y += z;
+    }
+    s_warp[lane] = y;
+  }
+  __syncthreads();
+  const int64_t first = x - pad + (warp > 0 ? s_warp[warp - 1] : 0);
+  const bool fits = s_warp[kSortWarps - 1] <= l_cap;
+  if (tid < E) {
+    s_next[tid] += static_cast<int32_t>(first);     // fits: below 2^31; unused otherwise
+    if (g == 0) counts[tid] = fits ? static_cast<int32_t>(n) : 0;
+  }
+  if (!fits) {
+    if (g == 0 && tid == 0) raise_status(status, AVR_ERR_INVALID_ARG);
+    for (int64_t i = lo + tid; i < hi; i += kSortThreads) row[i] = -1;
+    return;
+  }
+  // rounds of 1024 consecutive slots: rank inside the warp, then the warps in order
+  uint16_t* mine = s_in + warp * E;
+  for (int64_t base = lo; base < hi; base += kSortThreads) {
+    for (int i = tid; i < kSortWarps * E; i += kSortThreads) s_in[i] = 0;
+    __syncthreads();
+    bool bad = false;
+    const int64_t i = base + tid;
+    const int e = slot_expert(ids, i, hi, E, bad);
+    const uint32_t same = __match_any_sync(kFull, e);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    if (e >= 0 && rank == 0) mine[e] = static_cast<uint16_t>(__popc(same));
+    __syncthreads();
+    if (tid < E) {
+      int32_t at = 0;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int32_t c = s_in[w * E + tid];
+        s_in[w * E + tid] = static_cast<uint16_t>(at);
+        at += c;
+      }
+      s_total[tid] = at;                      // this round's slots of the expert
+    }
+    __syncthreads();
+    if (i < hi) row[i] = e >= 0 ? s_next[e] + mine[e] + rank : -1;
+    __syncthreads();
+    if (tid < E) s_next[tid] += s_total[tid];
+  }
+}
+
+cudaError_t launch_sort(const int32_t* ids, int64_t slots, int E, int64_t l_cap, int32_t* counts, int32_t* row,
+                        int32_t* scratch, uint32_t* status, cudaStream_t s) {
+  const int G = sort_chunks(slots);
+  const int64_t per = (slots + G - 1) / G;
+  if (G > 1) {
+    cudaError_t e = launch_ex(sort_count_kernel, dim3(G), dim3(kSortThreads), 0, s, true, ids, slots, per, E, scratch,
+                              status);
+    if (e != cudaSuccess) return e;
+  }
+  const size_t smem = static_cast<size_t>(kSortWarps) * static_cast<size_t>(E) * sizeof(uint16_t);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(sort_place_kernel), smem);
+  if (e != cudaSuccess) return e;
+  return launch_ex(sort_place_kernel, dim3(G), dim3(kSortThreads), smem, s, true, ids, slots, per, E, l_cap,
+                   static_cast<const int32_t*>(scratch), counts, row, status);
+}
+
+// ---------------------------------------------------------------------------
+// dispatch, combine and their gradients.  All go token by token: a token's
+// row of X, Y or dY is moved once whatever k is, and the buffer's rows once
+// each.  A warp takes (token, strip of 32 lanes x kU 16-byte vectors).
+// ---------------------------------------------------------------------------
+constexpr int kPermThreads = 256;
+
+// the buffer row of slot (t, j), -1 for none
+__device__ __forceinline__ int64_t slot_row(const PermuteArgs& a, int64_t t, int j) {
+  const int32_t r = __ldg(a.row + t * a.k + j);
+  if (r >= a.l_cap) {
+    raise_status(a.status, AVR_ERR_INVALID_ARG);
+    return -1;
+  }
+  return r;
+}
+
+constexpr int kDispU = 4;
+
+__global__ void __launch_bounds__(kPermThreads) dispatch_kernel(const PermuteArgs a, int64_t V, int strips) {
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kPermThreads / 32);
+  const uint4* src = static_cast<const uint4*>(a.src);
+  uint4* dst = static_cast<uint4*>(a.dst);
+  for (int64_t task = static_cast<int64_t>(blockIdx.x) * (kPermThreads / 32) + (threadIdx.x >> 5);
+       task < a.T * strips; task += warps) {
+    const int64_t t = task / strips;
+    const int64_t v0 = (task % strips) * (32 * kDispU) + lane;
+    uint4 q[kDispU];
+#pragma unroll
+    for (int u = 0; u < kDispU; ++u)
+      if (v0 + 32 * u < V) q[u] = __ldg(src + t * V + v0 + 32 * u);
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t r = slot_row(a, t, j);
+      if (r < 0) continue;
+#pragma unroll
+      for (int u = 0; u < kDispU; ++u)
+        if (v0 + 32 * u < V) dst[r * V + v0 + 32 * u] = q[u];
+    }
+  }
+}
+
+constexpr int kCombU = 2;
+
+template <bool kBf16, bool kWeighted>
+__global__ void __launch_bounds__(kPermThreads) combine_kernel(const PermuteArgs a, int64_t V, int strips) {
+  constexpr int N = Vec<kBf16>::kN;
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kPermThreads / 32);
+  const uint4* src = static_cast<const uint4*>(a.src);
+  uint4* dst = static_cast<uint4*>(a.dst);
+  for (int64_t task = static_cast<int64_t>(blockIdx.x) * (kPermThreads / 32) + (threadIdx.x >> 5);
+       task < a.T * strips; task += warps) {
+    const int64_t t = task / strips;
+    const int64_t v0 = (task % strips) * (32 * kCombU) + lane;
+    float acc[kCombU][N] = {};
+#pragma unroll 4
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t r = slot_row(a, t, j);
+      if (r < 0) continue;
+      const float w = kWeighted ? __ldg(a.weights + t * a.k + j) : 1.0f;
+#pragma unroll
+      for (int u = 0; u < kCombU; ++u) {
+        if (v0 + 32 * u < V) {
+          float f[N];
+          unpack<kBf16>(__ldg(src + r * V + v0 + 32 * u), f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[u][i] = kWeighted ? fmaf(w, f[i], acc[u][i]) : acc[u][i] + f[i];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kCombU; ++u)
+      if (v0 + 32 * u < V) dst[t * V + v0 + 32 * u] = pack<kBf16>(acc[u]);
+  }
+}
+
+// One CTA per token: dY's row stays in L1 over the slots, and the dot products
+// of all slots are summed in the same order whatever the grid.
+constexpr int kBwdThreads = 128;
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kBwdThreads) combine_bwd_kernel(const PermuteArgs a, int64_t V) {
+  constexpr int N = Vec<kBf16>::kN;
+  __shared__ float s_dot[kBwdThreads / 32][kMaxSlots];
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint4* dy = static_cast<const uint4*>(a.src);
+  const uint4* yp = static_cast<const uint4*>(a.yp);
+  uint4* dst = static_cast<uint4*>(a.dst);
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t r = slot_row(a, t, j);
+      float dot = 0.0f;
+      if (r >= 0) {
+        const float w = __ldg(a.weights + t * a.k + j);
+        for (int64_t v = threadIdx.x; v < V; v += kBwdThreads) {
+          float d[N], y[N], o[N];
+          unpack<kBf16>(__ldg(dy + t * V + v), d);
+          unpack<kBf16>(__ldg(yp + r * V + v), y);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            dot = fmaf(d[i], y[i], dot);
+            o[i] = w * d[i];
+          }
+          dst[r * V + v] = pack<kBf16>(o);
+        }
+      }
+      dot = warp_sum(dot);
+      if (lane == 0) s_dot[warp][j] = dot;
+    }
+    __syncthreads();
+    if (threadIdx.x < a.k) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kBwdThreads / 32; ++w) sum += s_dot[w][threadIdx.x];
+      a.dweights[t * a.k + threadIdx.x] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+static unsigned perm_grid(int64_t tasks, const void* fn) {
+  const int64_t need = (tasks + kPermThreads / 32 - 1) / (kPermThreads / 32);
+  const int64_t most = static_cast<int64_t>(sm_count()) * blocks_per_sm(fn, kPermThreads, 0) * 4;
+  return static_cast<unsigned>(need < most ? need : most);
+}
+
+cudaError_t launch_dispatch(const PermuteArgs& a, cudaStream_t s) {
+  const int64_t V = a.H / (a.xt == AVR_BF16 ? 8 : 4);
+  const int strips = static_cast<int>((V + 32 * kDispU - 1) / (32 * kDispU));
+  return launch_ex(dispatch_kernel, dim3(perm_grid(a.T * strips, reinterpret_cast<const void*>(dispatch_kernel))),
+                   dim3(kPermThreads), 0, s, true, a, V, strips);
+}
+
+template <bool kBf16, bool kWeighted>
+static cudaError_t combine_t(const PermuteArgs& a, cudaStream_t s) {
+  const int64_t V = a.H / Vec<kBf16>::kN;
+  const int strips = static_cast<int>((V + 32 * kCombU - 1) / (32 * kCombU));
+  auto kern = combine_kernel<kBf16, kWeighted>;
+  return launch_ex(kern, dim3(perm_grid(a.T * strips, reinterpret_cast<const void*>(kern))), dim3(kPermThreads), 0, s,
+                   true, a, V, strips);
+}
+
+cudaError_t launch_combine(const PermuteArgs& a, cudaStream_t s) {
+  if (a.weights != nullptr) return a.xt == AVR_BF16 ? combine_t<true, true>(a, s) : combine_t<false, true>(a, s);
+  return a.xt == AVR_BF16 ? combine_t<true, false>(a, s) : combine_t<false, false>(a, s);
+}
+
+template <bool kBf16>
+static cudaError_t combine_bwd_t(const PermuteArgs& a, cudaStream_t s) {
+  auto kern = combine_bwd_kernel<kBf16>;
+  const int64_t most = static_cast<int64_t>(sm_count()) *
+                       blocks_per_sm(reinterpret_cast<const void*>(kern), kBwdThreads, 0) * 4;
+  return launch_ex(kern, dim3(static_cast<unsigned>(a.T < most ? a.T : most)), dim3(kBwdThreads), 0, s, true, a,
+                   a.H / Vec<kBf16>::kN);
+}
+
+cudaError_t launch_combine_bwd(const PermuteArgs& a, cudaStream_t s) {
+  return a.xt == AVR_BF16 ? combine_bwd_t<true>(a, s) : combine_bwd_t<false>(a, s);
+}
+
+}  // namespace avr

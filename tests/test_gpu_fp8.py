@@ -1,0 +1,364 @@
+"""The 8-bit block products on the GPU against plain 64-bit forms: codes and
+scales bit for bit, products within the fp32 accumulation bound."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_io as R
+from quantized_gemm_column_b200 import inputs
+
+pytestmark = pytest.mark.gpu
+
+EPS = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}    # half a step, relative to the value
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def api():
+    from quantized_gemm_column_b200 import api as a
+    a.load()
+    return a
+
+
+def _x(l, K, dt, seed=0, spread=True):
+    """Values whose blocks have scales of very different sizes."""
+    rng = inputs.rng_for(210, seed)
+    x = rng.standard_normal((l, K))
+    if spread:
+        x *= 2.0 ** rng.integers(-12, 13, (l, -(-K // 128))).repeat(128, 1)[:, :K]
+    return torch.tensor(x, dtype=torch.float32).to(DT[dt])
+
+
+def _check_product(Y, a, b, K):
+    """Y [M, N] against a b^T in fp64: each of the K products is exact in fp32
+    (8 significand bits); the sums err by at most K 2^-24 of the magnitudes'
+    sum; then one rounding to Y's type."""
+    ref, mag = a @ b.T, np.abs(a) @ np.abs(b).T
+    tol = K * 2.0 ** -24 * mag + EPS[Y.dtype] * np.abs(ref)
+    got = Y.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4], float((np.abs(got - ref) / (tol + 1e-300)).max()))
+
+
+def _equal(t, q, s, rows=None):
+    """Codes and scales of an FP8Tensor against values and scale bytes."""
+    pick = slice(None) if rows is None else rows
+    got = R.e4m3_decode(t.codes.cpu().numpy())
+    assert np.array_equal(got[pick], q[pick])
+    assert np.array_equal(np.signbit(got[pick]), np.signbit(q[pick]))
+    if rows is None:
+        assert np.array_equal(t.scales.cpu().numpy(), R.atoms(s))
+    else:
+        assert np.array_equal(R.from_atoms(t.scales.cpu().numpy(), t.rows, s.shape[1])[pick], s[pick])
+
+
+# ---------------------------------------------------------------------------
+# quantizers
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("l,K", [(1, 16), (1, 128), (3, 144), (128, 512), (129, 528), (257, 1040), (1000, 64)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_quant_bit_exact(api, l, K, dt):
+    X = _x(l, K, dt, l + K)
+    out, ws = api.FP8Tensor(l, K), api.fp8_workspace(l, K, 16)
+    out.scales.fill_(0xEE)
+    api.fp8_quant(X.cuda(), out, ws)
+    assert api.averis_check_status(ws) == 0
+    _equal(out, *R.quant(X.double().numpy()))
+
+
+@pytest.mark.parametrize("l,K", [(1, 16), (128, 64), (129, 48), (300, 144), (513, 272), (640, 1040)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_quant_t_bit_exact(api, l, K, dt):
+    X = _x(l, K, dt, l + K)
+    L = -(-l // 128) * 128
+    out, ws = api.FP8Tensor(K, L), api.fp8_workspace(l, K, 16)
+    out.scales.fill_(0xEE)
+    api.fp8_quant_t(X.cuda(), out, ws)
+    assert api.averis_check_status(ws) == 0
+    full = np.zeros((K, L))
+    full[:, :l] = X.double().numpy().T
+    _equal(out, *R.quant(full))
+
+
+@pytest.mark.parametrize("m,n", [(16, 16), (128, 128), (144, 272), (1040, 2000), (512, 640)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_quant_weight_bit_exact(api, m, n, dt):
+    W = _x(m, n, dt, m + n)
+    f, d, ws = api.FP8Tensor(n, m), api.FP8Tensor(m, n), api.fp8_workspace(1, m, n)
+    f.scales.fill_(0xEE), d.scales.fill_(0xEE)
+    api.fp8_quant_weight(W.cuda(), f, d, ws)
+    f2 = api.FP8Tensor(n, m)
+    api.fp8_quant_weight(W.cuda(), f2, None, ws)                  # the forward's alone
+    assert api.averis_check_status(ws) == 0
+    q, s = R.quant(W.double().numpy(), (128, 128))
+    _equal(d, q, s.repeat(128, 0)[:m])
+    for t in (f, f2):
+        _equal(t, np.ascontiguousarray(q.T), np.ascontiguousarray(s.T.repeat(128, 0)[:n]))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_quant_special_blocks(api, dt):
+    """Zero blocks, both zeros, the exact edges of a scale step, the type's
+    largest and smallest values, ties of the code's rounding."""
+    lo, hi = torch.finfo(DT[dt]).smallest_normal, torch.finfo(DT[dt]).max
+    X = torch.zeros(12, 256)
+    X[1, 5] = -0.0
+    X[2, :128] = 448.0
+    X[2, 128:] = 449.0 if dt == "f32" else 450.0
+    X[3, 0], X[3, 128] = 2.0 ** -130, 2.0 ** -133               # subnormal amax
+    X[4, 0], X[4, 1], X[4, 128], X[4, 129] = hi, -hi, lo, lo / 2
+    X[5] = torch.linspace(-1, 1, 256)
+    X[6, 0] = 448.0
+    X[6, 1:100] = torch.arange(1, 100) * 2.0 ** -10              # ties among the subnormal codes
+    X[7, 0] = 1.75 * 2.0 ** 20
+    X[8, 0] = (1.75 + 2.0 ** -7) * 2.0 ** 20
+    X[9, 0] = 448.0
+    X[9, 1:120] = torch.arange(17, 136).float()                  # ties between codes
+    X[10, 0], X[10, 1] = 2.0 ** 100, 2.0 ** -100                  # vanishes beside the block's largest
+    X[11] = -448.0 * 2.0 ** -127
+    X = X.to(DT[dt])
+    out, ws = api.FP8Tensor(12, 256), api.fp8_workspace(12, 256, 128)
+    api.fp8_quant(X.cuda(), out, ws)
+    assert api.averis_check_status(ws) == 0
+    _equal(out, *R.quant(X.double().numpy()))
+    ot = api.FP8Tensor(256, 128)
+    api.fp8_quant_t(X.cuda(), ot, ws)
+    full = np.zeros((256, 128))
+    full[:, :12] = X.double().numpy().T
+    _equal(ot, *R.quant(full))
+    wf, wd = api.FP8Tensor(256, 16), api.FP8Tensor(16, 256)
+    W = torch.zeros(16, 256, dtype=DT[dt])
+    W[:12] = X
+    api.fp8_quant_weight(W.cuda(), wf, wd, ws)
+    q, s = R.quant(W.double().numpy(), (128, 128))
+    _equal(wd, q, s.repeat(128, 0)[:16])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_quant_non_finite_latches(api, value, dt):
+    X = _x(130, 272, dt)
+    X[129, 271] = value
+    ws = api.fp8_workspace(130, 272, 272)
+    for call in (lambda: api.fp8_quant(X.cuda(), api.FP8Tensor(130, 272), ws),
+                 lambda: api.fp8_quant_t(X.cuda(), api.FP8Tensor(272, 256), ws),
+                 lambda: api.fp8_quant_weight(X[2:].contiguous().cuda(), api.FP8Tensor(272, 128), None, ws)):
+        call()
+        assert api.averis_check_status(ws) == api.AVR_ERR_NONFINITE
+    api.fp8_quant(_x(130, 272, dt).cuda(), api.FP8Tensor(130, 272), ws)
+    assert api.averis_check_status(ws) == 0
+
+
+# ---------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("M,N,K", [(128, 256, 128), (256, 256, 512), (1, 16, 16), (1, 256, 640), (130, 272, 144),
+                                   (257, 528, 1040), (300, 128, 2064), (700, 1040, 4096), (64, 2304, 384),
+                                   (2500, 2320, 272)])
+@pytest.mark.parametrize("yt", ["f32", "bf16"])
+def test_gemm_matches_fp64(api, M, N, K, yt):
+    a, b, ws = api.FP8Tensor(M, K), api.FP8Tensor(N, K), api.fp8_workspace(max(M, N), K, 16)
+    api.fp8_quant(_x(M, K, "f32", 1, spread=K <= 640).cuda(), a, ws)
+    api.fp8_quant(_x(N, K, "f32", 2, spread=K <= 640).cuda(), b, ws)
+    Y = torch.full((M, N), 7.0, dtype=DT[yt], device="cuda")
+    api.fp8_gemm(a, b, Y, ws)
+    assert api.averis_check_status(ws) == 0
+    _check_product(Y, R.tensor_value(a), R.tensor_value(b), K)
+
+
+def test_gemm_places_every_code_and_scale(api):
+    """A = rows of a unit matrix picks B's elements one by one, each with the
+    scales of its row and block: exact."""
+    M = K = 1040
+    N = 272
+    a, b, ws = api.FP8Tensor(M, K), api.FP8Tensor(N, K), api.fp8_workspace(M, K, 16)
+    A = torch.eye(M, K) * (2.0 ** ((torch.arange(M) % 23) - 11.0))[:, None]
+    api.fp8_quant(A.cuda(), a, ws)
+    api.fp8_quant(_x(N, K, "f32", 6).cuda(), b, ws)
+    Y = torch.empty(M, N, device="cuda")
+    api.fp8_gemm(a, b, Y, ws)
+    assert api.averis_check_status(ws) == 0
+    assert np.array_equal(Y.double().cpu().numpy(), R.tensor_value(a) @ R.tensor_value(b).T)
+
+
+def _weights(api, m, n, dt, seed, ws):
+    W = _x(m, n, dt, seed, spread=False)
+    f, d = api.FP8Tensor(n, m), api.FP8Tensor(m, n)
+    api.fp8_quant_weight(W.cuda(), f, d, ws)
+    return R.deq(W.double().numpy(), (128, 128)), f, d
+
+
+@pytest.mark.parametrize("l,m,n", [(1, 16, 16), (1, 1024, 640), (2, 144, 272), (17, 256, 2064), (129, 1040, 400),
+                                   (1000, 272, 528)])
+@pytest.mark.parametrize("dt,ot", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16")])
+def test_linear_forward_and_gradients(api, l, m, n, dt, ot):
+    ws = api.fp8_workspace(l, m, n)
+    w, f, d = _weights(api, m, n, dt, m + n, ws)
+    X, D = _x(l, m, dt, 3, spread=False), _x(l, n, dt, 4, spread=False)
+    new = lambda *s: torch.full(s, 7.0, dtype=DT[ot], device="cuda")     # noqa: E731
+    Y, dX, dW = new(l, n), new(l, m), new(m, n)
+    api.fp8_linear_fwd(X.cuda(), f, Y, ws)
+    api.fp8_linear_dgrad(D.cuda(), d, dX, ws)
+    api.fp8_linear_wgrad(X.cuda(), D.cuda(), dW, ws)
+    assert api.averis_check_status(ws) == 0
+    x, dd = X.double().numpy(), D.double().numpy()
+    _check_product(Y, R.deq(x), w.T, m)
+    _check_product(dX, R.deq(dd), w, n)
+    _check_product(dW, R.deq(x.T.copy()), R.deq(dd.T.copy()), l)
+
+
+def test_linear_no_tokens(api):
+    ws = api.fp8_workspace(0, 64, 32)
+    z = lambda *s: torch.zeros(*s, device="cuda")                        # noqa: E731
+    f, d = api.FP8Tensor(32, 64), api.FP8Tensor(64, 32)
+    api.fp8_linear_fwd(z(0, 64), f, z(0, 32), ws)
+    api.fp8_linear_dgrad(z(0, 32), d, z(0, 64), ws)
+    dW = torch.full((64, 32), 7.0, device="cuda")
+    api.fp8_linear_wgrad(z(0, 64), z(0, 32), dW, ws)
+    assert api.averis_check_status(ws) == 0 and not dW.any()
+
+
+def test_gradients_against_differences(api):
+    """sum(D * Q(X) W) is linear in W: its derivative along V is the inner
+    product of V with Q(X)^T D, which dW approximates to the codes' rounding
+    (half a step of E4M3, 2^-4, for X and D each)."""
+    l, m, n = 200, 144, 80
+    ws = api.fp8_workspace(l, m, n)
+    X, D, V = _x(l, m, "f32", 1, spread=False), _x(l, n, "f32", 2, spread=False), _x(m, n, "f32", 3, spread=False)
+    dW = torch.empty(m, n, device="cuda")
+    api.fp8_linear_wgrad(X.cuda(), D.cuda(), dW, ws)
+    x, d, v = X.double().numpy(), D.double().numpy(), V.double().numpy()
+    h = 0.5
+    diff = ((d * (x @ (h * v))).sum() - (d * (x @ (-h * v))).sum()) / (2 * h)
+    bound = (2 * 2.0 ** -4 + 2.0 ** -8) * (np.abs(x).T @ np.abs(d) * np.abs(v)).sum()
+    assert abs((dW.double().cpu().numpy() * v).sum() - diff) <= bound
+    # and element by element
+    el = (2 * 2.0 ** -4 + 2.0 ** -8) * (np.abs(x).T @ np.abs(d)) + l * 2.0 ** -8
+    assert np.all(np.abs(dW.double().cpu().numpy() - x.T @ d) <= el)
+
+
+# ---------------------------------------------------------------------------
+# experts
+# ---------------------------------------------------------------------------
+COUNTS = [[300, 0, 129, 1, 512, 64], [1], [0, 0, 5], [128, 128, 256], [0, 700, 33], [31, 32, 33, 97, 127, 255, 257]]
+
+
+def _segments(counts):
+    off, o = [], 0
+    for c in counts:
+        off.append(o)
+        o += -(-c // 128) * 128
+    return off, o
+
+
+def _buffer(counts, K, dt, seed, extra=128):
+    """Rows of every expert; the rows without a token hold NaN, which nothing may read."""
+    off, used = _segments(counts)
+    X = torch.full((used + extra, K), float("nan")).to(DT[dt])
+    rng = inputs.rng_for(211, seed)
+    for o, c in zip(off, counts):
+        X[o:o + c] = torch.tensor(rng.standard_normal((c, K)), dtype=torch.float32).to(DT[dt])
+    return X, off
+
+
+def _experts(api, E, m, n, dt, ws, seed=0):
+    W = torch.stack([_x(m, n, dt, seed + e, spread=False) * 2.0 ** e for e in range(E)])
+    f, d = api.FP8Tensor(E * n, m), api.FP8Tensor(E * m, n)
+    api.fp8_moe_quant_weights(W.cuda(), f, d, ws)
+    return [R.deq(W[e].double().numpy(), (128, 128)) for e in range(E)], f, d
+
+
+@pytest.mark.parametrize("counts", COUNTS)
+@pytest.mark.parametrize("m,n,dt,ot", [(256, 384, "bf16", "bf16"), (128, 128, "f32", "f32"), (640, 256, "bf16", "f32")])
+def test_experts_forward_and_gradients(api, counts, m, n, dt, ot):
+    E = len(counts)
+    X, off = _buffer(counts, m, dt, 1)
+    D, _ = _buffer(counts, n, dt, 2)
+    cap = X.shape[0]
+    ws = api.fp8_moe_workspace(cap, m, n, E)
+    w, f, d = _experts(api, E, m, n, dt, ws)
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    new = lambda *s: torch.full(s, 7.0, dtype=DT[ot], device="cuda")     # noqa: E731
+    Y, dX, dW = new(cap, n), new(cap, m), new(E, m, n)
+    api.fp8_moe_linear_fwd(X.cuda(), cnt, f, Y, ws)
+    api.fp8_moe_linear_dgrad(D.cuda(), cnt, d, dX, ws)
+    api.fp8_moe_linear_wgrad(X.cuda(), D.cuda(), cnt, dW, ws)
+    assert api.averis_check_status(ws) == 0
+    free = np.ones(cap, dtype=bool)
+    for e, (o, c) in enumerate(zip(off, counts)):
+        free[o:o + c] = False
+        if c == 0:
+            assert not dW[e].any()
+            continue
+        x, dd = X[o:o + c].double().numpy(), D[o:o + c].double().numpy()
+        _check_product(Y[o:o + c], R.deq(x), w[e].T, m)
+        _check_product(dX[o:o + c], R.deq(dd), w[e], n)
+        _check_product(dW[e], R.deq(x.T.copy()), R.deq(dd.T.copy()), c)
+    assert (Y[torch.from_numpy(free)] == 7.0).all() and (dX[torch.from_numpy(free)] == 7.0).all()
+
+
+def test_experts_weights_bit_exact(api):
+    E, m, n = 3, 256, 384
+    ws = api.fp8_moe_workspace(0, m, n, E)
+    W = torch.stack([_x(m, n, "bf16", e) for e in range(E)])
+    f, d, f2 = api.FP8Tensor(E * n, m), api.FP8Tensor(E * m, n), api.FP8Tensor(E * n, m)
+    api.fp8_moe_quant_weights(W.cuda(), f, d, ws)
+    api.fp8_moe_quant_weights(W.cuda(), f2, None, ws)
+    assert api.averis_check_status(ws) == 0
+    qs = [R.quant(W[e].double().numpy(), (128, 128)) for e in range(E)]
+    _equal(d, np.concatenate([q for q, _ in qs]), np.concatenate([s.repeat(128, 0) for _, s in qs]))
+    for t in (f, f2):
+        _equal(t, np.concatenate([q.T for q, _ in qs]), np.concatenate([s.T.repeat(128, 0) for _, s in qs]))
+
+
+@pytest.mark.parametrize("bad", [[200, 300], [-1, 5], [2 ** 31 - 1, 2 ** 31 - 1], [400, 0]])
+def test_experts_counts_that_do_not_fit(api, bad):
+    E, cap, m = 2, 384, 128
+    ws = api.fp8_moe_workspace(cap, m, m, E)
+    _, f, d = _experts(api, E, m, m, "bf16", ws)
+    X = torch.ones(cap, m, dtype=torch.bfloat16, device="cuda")
+    Y, dW = torch.full_like(X, 7.0), torch.full((E, m, m), 7.0, device="cuda")
+    cnt = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    for call in (lambda: api.fp8_moe_linear_fwd(X, cnt, f, Y, ws), lambda: api.fp8_moe_linear_dgrad(X, cnt, d, Y, ws),
+                 lambda: api.fp8_moe_linear_wgrad(X, X, cnt, dW, ws),
+                 lambda: api.fp8_moe_gemm(api.FP8Tensor(cap, m), cnt, f, Y, ws)):
+        call()
+        assert api.averis_check_status(ws) == api.AVR_ERR_INVALID_ARG
+    assert (Y == 7.0).all() and (dW == 7.0).all()
+    api.fp8_moe_linear_fwd(X, torch.tensor([256, 128], dtype=torch.int32, device="cuda"), f, Y, ws)
+    assert api.averis_check_status(ws) == 0 and (Y != 7.0).all()
+
+
+def test_experts_empty_buffer(api):
+    E, m = 3, 128
+    ws = api.fp8_moe_workspace(0, m, m, E)
+    _, f, _ = _experts(api, E, m, m, "bf16", ws)
+    z, cnt = torch.zeros(0, m, dtype=torch.bfloat16, device="cuda"), torch.zeros(E, dtype=torch.int32, device="cuda")
+    dW = torch.full((E, m, m), 7.0, device="cuda")
+    api.fp8_moe_linear_fwd(z, cnt, f, z, ws)
+    api.fp8_moe_linear_wgrad(z, z, cnt, dW, ws)
+    assert api.averis_check_status(ws) == 0 and not dW.any()
+
+
+@pytest.mark.parametrize("T,k,E,K", [(1, 8, 64, 128), (50, 4, 6, 640), (300, 2, 3, 512)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_dispatch_quantizes_the_tokens_rows(api, T, k, E, K, dt):
+    ids = inputs.rng_for(212, T).integers(-1, E, (T, k)).astype(np.int32)
+    _, row, _, _ = R.sort(ids, E)
+    cap = api.moe_max_rows(T, k, E)
+    X = _x(T, K, dt, 5)
+    xq, ws = api.FP8Tensor(cap, K), api.fp8_moe_workspace(cap, K, 128, E)
+    xq.codes.fill_(0x55), xq.scales.fill_(0x55)
+    api.fp8_moe_dispatch(X.cuda(), torch.from_numpy(row.astype(np.int32)).cuda(), xq, ws)
+    assert api.averis_check_status(ws) == 0
+    q, s = R.quant(X.double().numpy())
+    wq, wsb = np.full((cap, K), R.e4m3_decode([0x55])[0]), np.full((cap, K // 128), 0x55, dtype=np.uint8)
+    for i, j in zip(*np.nonzero(row >= 0)):
+        wq[row[i, j]], wsb[row[i, j]] = q[i], s[i]
+    _equal(xq, wq, wsb, rows=np.arange(cap))
+    bad = torch.full((T, k), cap, dtype=torch.int32, device="cuda")      # past the buffer: skipped, latched
+    api.fp8_moe_dispatch(X.cuda(), bad, xq, ws)
+    assert api.averis_check_status(ws) == api.AVR_ERR_INVALID_ARG
+    _equal(xq, wq, wsb, rows=np.arange(cap))
