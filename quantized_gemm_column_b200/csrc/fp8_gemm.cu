@@ -9,15 +9,18 @@
 // instructions that read the same byte.  A scale word in tensor memory has
 // four bytes and the instruction descriptor picks one, so a 512-byte atom
 // (128 rows x 4 blocks) serves 512 of K: three copies of scales (one of A's
-// atoms, two of B's) per 16 MMAs, which the MMA thread issues itself.
+// atoms, two of B's) per 16 MMAs.
 //
 // Persistent CTA pairs (cta_group::2) on 256 x 256 tiles, as the FP4 pair
 // kernel: each CTA holds its 128 rows of A and half of B, so an SM loads 32 KB
 // for the 2 * 128 * 256 * 128 flop of its share of a stage.
 //   warp 0      : tensor-memory allocation; in the leading CTA one thread
-//                 copies scales and issues the pair's MMAs;
+//                 issues the pair's MMAs;
 //   warps 1..4  : TMA producers of A and B, two each, alternate stages;
 //   warp 5      : producer of the scale atoms, two slots of 512 of K;
+//   warp 6      : in the leading CTA one thread copies the scales into tensor
+//                 memory, a slot ahead of the MMAs, which would wait for
+//                 copies of their own thread;
 //   warps 8..15 : epilogue, each a lane quarter of one 128-column half, through
 //                 a 4 KB staging box of its own and a TMA store.
 //
@@ -52,6 +55,7 @@ struct Cfg {
   static constexpr int kSfaBytes = 512, kSfbBytes = 1024;
   static constexpr int kProducers = 4;
   static constexpr int kScaleWarp = 1 + kProducers;
+  static constexpr int kCopyWarp = kScaleWarp + 1;
   static constexpr int kFirstEpiWarp = 8, kEpiWarps = 8;
   static constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
   static constexpr int kBoxBytes = 32 * 128;                    // an epilogue warp's staging box
@@ -144,6 +148,16 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// One lane of a converged warp.  The compiler knows that the branch on it has
+// one thread, which a branch on the lane number does not tell it: issued from
+// the latter, the MMAs, commits and copies of a stage took about 290 ns more
+// (8192 x 1024 x 4096: 36.8 -> 27.6 us).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void mma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
   asm volatile(
@@ -175,10 +189,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
   uint64_t* empty = full + Cfg::kStages;        // [kStages] both CTAs
   uint64_t* sf_full = empty + Cfg::kStages;     // [kSlots] leading CTA: scale atoms landed in both CTAs
   uint64_t* sf_empty = sf_full + Cfg::kSlots;   // [kSlots] both CTAs
-  uint64_t* acc_full = sf_empty + Cfg::kSlots;  // both CTAs
+  uint64_t* sf_ready = sf_empty + Cfg::kSlots;  // [kSlots] leading CTA: in tensor memory
+  uint64_t* acc_full = sf_ready + Cfg::kSlots;  // both CTAs
   uint64_t* acc_empty = acc_full + 1;           // leading CTA: every epilogue warp of both
-  uint64_t* drained = acc_empty + 1;            // leading CTA
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  uint64_t* drained = acc_empty + 1;            // [2] leading CTA: the MMA and copy threads'
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -198,10 +213,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
     for (int s = 0; s < Cfg::kSlots; ++s) {
       mbar_init(&sf_full[s], 1);
       mbar_init(&sf_empty[s], 1);
+      mbar_init(&sf_ready[s], 1);
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 2 * Cfg::kEpiWarps);
-    mbar_init(drained, 1);
+    mbar_init(&drained[0], 1);
+    mbar_init(&drained[1], 1);
     fence_mbarrier_init();
   }
   if (warp == 0) {
@@ -225,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
   if (!aligned) num_tiles = 0;
 
   if (warp >= 1 && warp <= Cfg::kProducers) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---------------- A and B producers ----------------
       const bool is_a = warp <= 2;
       const int parity = (warp - 1) & 1;
@@ -238,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
           if ((it & 1) != parity) continue;
           const int st = it % Cfg::kStages;
           const uint32_t ph = static_cast<uint32_t>(it / Cfg::kStages) & 1u;
-          if (it >= Cfg::kStages && !mbar_wait(&empty[st], ph ^ 1u, p.status)) {
+          if (it >= Cfg::kStages && !mbar_wait_backoff(&empty[st], ph ^ 1u, p.status)) {
             ok = false;
             break;
           }
@@ -252,7 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
       }
     }
   } else if (warp == Cfg::kScaleWarp) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---------------- scale producer: the atoms of 512 of K ----------------
       const uint32_t bar_lead = mapa_shared(smem_u32(sf_full), 0);
       int it = 0;
@@ -274,12 +291,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
         }
       }
     }
-  } else if (warp == 0) {
-    if (lead && lane == 0) {
-      // ---------------- MMA issuer (leading CTA) ----------------
-      // Copies of scales and MMAs of one thread run in order.  A slot's
-      // tensor-memory columns are free when its shared memory is: the
+  } else if (warp == Cfg::kCopyWarp) {
+    if (lead && elect_one()) {
+      // ---------------- scale copier (leading CTA; each copy fills both CTAs) ----------------
+      // A slot's tensor-memory columns are free when its shared memory is: the
       // producer refilled it after the MMAs that read both had completed.
+      int it = 0;
+      bool ok = true;
+      for (int i = pair; i < num_tiles && ok; i += pairs) {
+        const Tile t = tile_at<kMode>(p, i, 0);
+        if (t.nkb == 0) continue;
+        for (int c = t.kb0 >> 2; c <= (t.kb0 + t.nkb - 1) >> 2; ++c, ++it) {
+          const int sl = it % Cfg::kSlots;
+          if (!mbar_wait_poll(&sf_full[sl], static_cast<uint32_t>(it / Cfg::kSlots) & 1u, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = smem_desc(smem_u32(sSfa + sl * Cfg::kSfaBytes), 0, 128, kLayoutSwizzleNone);
+          const uint64_t db = smem_desc(smem_u32(sSfb + sl * Cfg::kSfbBytes), 0, 128, kLayoutSwizzleNone);
+          const uint32_t sfb_t = tmem + Cfg::kSfbCol + 8 * sl;
+          tc_cp_32x128b_warpx4_pair(tmem + Cfg::kSfaCol + 4 * sl, da);
+          tc_cp_32x128b_warpx4_pair(sfb_t, db);
+          tc_cp_32x128b_warpx4_pair(sfb_t + 4, db + 32);
+          tc_commit_pair(&sf_ready[sl]);
+        }
+      }
+      tc_commit_pair(&drained[1]);
+      mbar_wait(&drained[1], 0, p.status);
+    }
+  } else if (warp == 0) {
+    if (lead && elect_one()) {
+      // ---------------- MMA issuer (leading CTA) ----------------
       int st = 0, sl = 0, done = 0;
       uint32_t ph = 0, sph = 0;
       bool ok = true;
@@ -291,16 +334,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
         for (int kb = t.kb0; kb < end; ++kb) {
           const uint32_t sfa_t = tmem + Cfg::kSfaCol + 4 * sl, sfb_t = tmem + Cfg::kSfbCol + 8 * sl;
           if (kb == t.kb0 || (kb & 3) == 0) {
-            if (!mbar_wait_poll(&sf_full[sl], sph, p.status)) {
+            if (!mbar_wait_poll(&sf_ready[sl], sph, p.status)) {
               ok = false;
               break;
             }
-            tc_fence_after();
-            const uint64_t da = smem_desc(smem_u32(sSfa + sl * Cfg::kSfaBytes), 0, 128, kLayoutSwizzleNone);
-            const uint64_t db = smem_desc(smem_u32(sSfb + sl * Cfg::kSfbBytes), 0, 128, kLayoutSwizzleNone);
-            tc_cp_32x128b_warpx4_pair(sfa_t, da);
-            tc_cp_32x128b_warpx4_pair(sfb_t, db);
-            tc_cp_32x128b_warpx4_pair(sfb_t + 4, db + 32);
           }
           if (!mbar_wait_poll(&full[st], ph, p.status) ||
               (kb == t.kb0 && done >= 1 &&
@@ -334,8 +371,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
         tc_commit_pair_both(acc_full);
         ++done;
       }
-      tc_commit_pair(drained);
-      mbar_wait(drained, 0, p.status);
+      tc_commit_pair(&drained[0]);
+      mbar_wait(&drained[0], 0, p.status);
     }
   } else if (warp >= Cfg::kFirstEpiWarp) {
     // ---------------- epilogue (both CTAs, own rows) ----------------
@@ -360,34 +397,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
                              static_cast<uint32_t>(Cfg::kAccStep * (done & 1) + 128 * h);
       const int rows = t.rows - 32 * q;                    // of this warp's 32
       const int64_t y_row = t.y_row + 32 * q;
+      // The columns shared with the next tile come out first: the last 32 of a
+      // tile at column 0 (half 1), the first 32 of one at 224 (half 0).  Every
+      // warp arrives once a tile, its tile before done: then the next MMAs may write.
+      const bool odd = (done & 1) != 0;
+      bool owe = has;
+      auto release = [&]() {
+        if (owe) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty_lead);
+          owe = false;
+        }
+      };
+      if (h != (odd ? 0 : 1)) release();
       for (int b = 0; b < kBoxes; ++b) {
-        // the columns shared with the next tile come out first: the last 32 of
-        // a tile at column 0, the first 32 of one at 224
-        const int bx = (done & 1) ? b : kBoxes - 1 - b;
+        const int bx = odd ? b : kBoxes - 1 - b;
         uint32_t w[32];
         if (has) {
           if (kBf16Out) {
-            uint32_t v0[32], v1[32];
-            tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(64 * bx), v0);
-            tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(64 * bx + 32), v1);
-            tmem_ld_wait();
+            // 32 columns as 16 bf16 pairs
+            auto load_pack = [&](int half) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(64 * bx + 32 * half), v);
+              tmem_ld_wait();
+              release();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const __nv_bfloat162 lo = __floats2bfloat162_rn(__uint_as_float(v0[2 * k]), __uint_as_float(v0[2 * k + 1]));
-              const __nv_bfloat162 hi = __floats2bfloat162_rn(__uint_as_float(v1[2 * k]), __uint_as_float(v1[2 * k + 1]));
-              w[k] = *reinterpret_cast<const uint32_t*>(&lo);
-              w[16 + k] = *reinterpret_cast<const uint32_t*>(&hi);
+              for (int k = 0; k < 16; ++k) {
+                const __nv_bfloat162 pr = __floats2bfloat162_rn(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+                w[16 * half + k] = *reinterpret_cast<const uint32_t*>(&pr);
+              }
+            };
+            if (odd) {
+              load_pack(0);
+              load_pack(1);
+            } else {
+              load_pack(1);
+              load_pack(0);
             }
           } else {
             tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(32 * bx), w);
             tmem_ld_wait();
-          }
-          if (b == 0) {
-            // every warp's first box is out, and all of the tile before: the
-            // next tile's MMAs may write
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty_lead);
+            release();
           }
         } else {
 #pragma unroll
