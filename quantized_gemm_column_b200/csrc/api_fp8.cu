@@ -97,6 +97,7 @@ Fp8GemmArgs gemm_args(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a
   g.Y = Y;
   g.y_rows = y_rows;
   g.yt = yt;
+  g.flags = at<uint32_t>(ws, WsLayout{}.tickets);
   g.status = status_of(ws);
   return g;
 }

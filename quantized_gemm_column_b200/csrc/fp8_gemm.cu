@@ -30,6 +30,18 @@
 // then lets the next tile's MMAs start, so the rest of the drain, the
 // conversion and the stores run under them.
 //
+// The tensor core's fp32 sums are cut off, not rounded, so a long sum of one
+// sign drifts (1e-6 relative over 4096 terms, 9e-6 over 16384).  An fp32
+// output is therefore summed in visits of at most 4096 of K: the first is
+// stored, the others are added to it by TMA reductions, which round to nearest,
+// in order.  A bf16 output's own rounding is 400 times that drift.
+//
+// When the last round of an fp32 output has tiles for less than half of the
+// pairs, each of them is cut along K among several pairs (parts).  A part adds
+// to what the part below it has stored: it waits for a pair of lower index,
+// which the hardware starts no later, in the same round.  So the order of the
+// additions, and the bits, are fixed.
+//
 // Three uses, one code path: one product; the experts' buffer by row tiles
 // (kRows: a tile's rows belong to one expert, whose B is stacked); the
 // experts' weight gradients (kTokens: one product per expert, K = its tokens,
@@ -47,6 +59,8 @@ using namespace pair;
 
 namespace {
 
+constexpr int kMinPart = 12;
+
 struct Cfg {
   static constexpr int kBM = 128, kBN = 256, kBNHalf = 128;     // per CTA; a pair's tile is 256 x 256
   static constexpr int kStages = 5;                             // 128 of K each
@@ -59,6 +73,7 @@ struct Cfg {
   static constexpr int kFirstEpiWarp = 8, kEpiWarps = 8;
   static constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
   static constexpr int kBoxBytes = 32 * 128;                    // an epilogue warp's staging box
+  static constexpr int kMaxVisit = 48;                          // blocks of K in one fp32 visit
   static constexpr int kOutOffset = kStages * (kABytes + kBBytes);
   static constexpr int kSfaOffset = kOutOffset + kEpiWarps * kBoxBytes;
   static constexpr int kSfbOffset = kSfaOffset + kSlots * kSfaBytes;
@@ -81,9 +96,11 @@ struct Params {
   int64_t M, N;
   int tiles_m, tiles_n, nkb;      // kTokens: per expert, nkb unused
   int num_tiles;                  // kRows: computed from the table's tile count
+  int cut0, parts;                // tiles from cut0 on are cut into parts (kDense, fp32; else past the end, 1)
   int a_oob;                      // a row coordinate past A: reads zeros
   Fp8Table t;
   void* Y;
+  uint32_t* flags;                // [pairs][2][8], zero between launches: a warp's share of a part is stored
   uint32_t* status;
 };
 
@@ -94,12 +111,23 @@ struct Tile {
   int32_t n0, kb0, nkb;
   int64_t y_row;
   int32_t rows;                   // rows of this CTA's 128 to be stored (<= 0: none)
+  int32_t part;                   // kDense: which part of the tile (0: all, or the first)
 };
 
 template <int kMode>
 __device__ __forceinline__ Tile tile_at(const Params& p, int i, int rank) {
   Tile t;
+  t.part = 0;
   if (kMode == Fp8GemmArgs::kDense) {
+    t.kb0 = 0;
+    t.nkb = p.nkb;
+    if (i >= p.cut0) {
+      const int item = i - p.cut0;
+      i = p.cut0 + item / p.parts;
+      t.part = item % p.parts;
+      t.kb0 = p.nkb * t.part / p.parts;
+      t.nkb = p.nkb * (t.part + 1) / p.parts - t.kb0;
+    }
     // bands of 8 column tiles, rows outside, so that the pairs working at one
     // time share both operands' tiles in L2
     const int band = i / (8 * p.tiles_m), r = i - band * 8 * p.tiles_m;
@@ -108,8 +136,6 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int i, int rank) {
     t.n0 = (8 * band + r % width) * 256;
     t.a_row = m0;
     t.b_row0 = t.n0;
-    t.kb0 = 0;
-    t.nkb = p.nkb;
     t.y_row = m0;
     t.rows = static_cast<int32_t>(min64(128, p.M - m0));
   } else if (kMode == Fp8GemmArgs::kRows) {
@@ -137,6 +163,13 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int i, int rank) {
   return t;
 }
 
+// blocks of K in a visit of a tile of n: n, or the fewest equal visits for fp32
+template <bool kBf16Out>
+__device__ __forceinline__ int visit_length(int n) {
+  const int visits = (n + Cfg::kMaxVisit - 1) / Cfg::kMaxVisit;
+  return kBf16Out || visits < 2 ? n : (n + visits - 1) / visits;
+}
+
 // TMA 2-D load into this CTA's shared memory, completing on the barrier at a
 // shared::cluster address in either CTA of the pair
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int32_t x,
@@ -156,6 +189,35 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
+}
+
+// TMA reduction shared -> global: adds, each element rounded to nearest
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%2, %3}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+}
+
+// a flag that a thread sets after its stores completed, and one of another CTA waits for and hands back
+__device__ __forceinline__ void flag_set(uint32_t* f) {
+  fence_proxy_async_global();
+  __threadfence();
+  asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(f) : "memory");
+}
+__device__ __forceinline__ bool flag_take(uint32_t* f, uint32_t* status) {
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    uint32_t x;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(f) : "memory");
+    if (x != 0u) break;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      raise_status(status, AVR_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+  }
+  *f = 0u;
+  fence_proxy_async_global();
+  return true;
 }
 
 __device__ __forceinline__ void mma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -329,9 +391,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
       for (int i = pair; i < num_tiles && ok; i += pairs) {
         const Tile t = tile_at<kMode>(p, i, 0);
         if (t.nkb == 0) continue;
-        const uint32_t d = tmem + static_cast<uint32_t>(Cfg::kAccStep * (done & 1));
+        uint32_t d = tmem + static_cast<uint32_t>(Cfg::kAccStep * (done & 1));
         const int end = t.kb0 + t.nkb;
+        const int visit = visit_length<kBf16Out>(t.nkb);
+        int kb0 = t.kb0;                        // the visit's first block
         for (int kb = t.kb0; kb < end; ++kb) {
+          if (!kBf16Out && kb == kb0 + visit) {
+            tc_commit_pair_both(acc_full);
+            ++done;
+            d = tmem + static_cast<uint32_t>(Cfg::kAccStep * (done & 1));
+            kb0 = kb;
+          }
           const uint32_t sfa_t = tmem + Cfg::kSfaCol + 4 * sl, sfb_t = tmem + Cfg::kSfbCol + 8 * sl;
           if (kb == t.kb0 || (kb & 3) == 0) {
             if (!mbar_wait_poll(&sf_ready[sl], sph, p.status)) {
@@ -340,7 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
             }
           }
           if (!mbar_wait_poll(&full[st], ph, p.status) ||
-              (kb == t.kb0 && done >= 1 &&
+              (kb == kb0 && done >= 1 &&
                !mbar_wait_poll(acc_empty, static_cast<uint32_t>(done - 1) & 1u, p.status))) {
             ok = false;
             break;
@@ -353,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             mma_fp8_pair(d, a0 + static_cast<uint64_t>(2 * q), b0 + static_cast<uint64_t>(2 * q), idesc, sfa_t, sfb_t,
-                         (kb > t.kb0 || q > 0) ? 1u : 0u);
+                         (kb > kb0 || q > 0) ? 1u : 0u);
           tc_commit_pair_both(&empty[st]);
           if ((kb & 3) == 3 || kb + 1 == end) {
             tc_commit_pair_both(&sf_empty[sl]);
@@ -383,38 +453,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
     constexpr int kBoxCols = kBf16Out ? 64 : 32;           // 128 bytes of output
     constexpr int kBoxes = 128 / kBoxCols;
     constexpr int kElem = kBf16Out ? 2 : 4;
-    int done = 0;
-    for (int i = pair; i < num_tiles; i += pairs) {
-      const Tile t = tile_at<kMode>(p, i, rank);
-      const bool has = t.nkb > 0;                          // an expert without tokens: a zero gradient
-      if (has) {
-        uint32_t okw = 0;
-        if (lane == 0) okw = mbar_wait_backoff(acc_full, static_cast<uint32_t>(done) & 1u, p.status) ? 1u : 0u;
-        if (__shfl_sync(0xFFFFFFFFu, okw, 0) == 0u) break;
-        tc_fence_after();
+    // 32 output words of a box go out, w[k] at column col + k of row `lane`; add: to what is there
+    auto store_box = [&](const uint32_t (&w)[32], int rows, int64_t y_row, int64_t col, bool add) {
+      if (rows <= 0 || col >= p.N) return;                 // the whole warp
+      if (kMode == Fp8GemmArgs::kRows && rows < 32) {
+        // the last rows of a segment: the rows behind them are not written
+        if (lane < rows) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.Y) + ((y_row + lane) * p.N + col) * kElem);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            if (col + u * (16 / kElem) >= p.N) continue;
+            uint4 x = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+            if (!kBf16Out && add) {
+              const uint4 y = dst[u];
+              x = make_uint4(__float_as_uint(__uint_as_float(y.x) + __uint_as_float(x.x)),
+                             __float_as_uint(__uint_as_float(y.y) + __uint_as_float(x.y)),
+                             __float_as_uint(__uint_as_float(y.z) + __uint_as_float(x.z)),
+                             __float_as_uint(__uint_as_float(y.w) + __uint_as_float(x.w)));
+            }
+            dst[u] = x;
+          }
+        }
+        return;
       }
-      const uint32_t t_row = tmem + (static_cast<uint32_t>(32 * q) << 16) +
-                             static_cast<uint32_t>(Cfg::kAccStep * (done & 1) + 128 * h);
+      if (lane == 0) bulk_wait_group_read<0>();            // the box's previous store has read it
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        *reinterpret_cast<uint4*>(box + lane * 128 + ((u ^ (lane & 7)) * 16)) =
+            make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {                                     // clipped at Y's edges
+        if (!kBf16Out && add)
+          tma_add_2d(&map_y, box, static_cast<int32_t>(col), static_cast<int32_t>(y_row));
+        else
+          tma_store_2d(&map_y, box, static_cast<int32_t>(col), static_cast<int32_t>(y_row));
+        bulk_commit_group();
+      }
+    };
+    int done = 0;
+    bool ok = true;
+    for (int i = pair; i < num_tiles && ok; i += pairs) {
+      const Tile t = tile_at<kMode>(p, i, rank);
       const int rows = t.rows - 32 * q;                    // of this warp's 32
       const int64_t y_row = t.y_row + 32 * q;
-      // The columns shared with the next tile come out first: the last 32 of a
-      // tile at column 0 (half 1), the first 32 of one at 224 (half 0).  Every
-      // warp arrives once a tile, its tile before done: then the next MMAs may write.
-      const bool odd = (done & 1) != 0;
-      bool owe = has;
-      auto release = [&]() {
-        if (owe) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(acc_empty_lead);
-          owe = false;
-        }
-      };
-      if (h != (odd ? 0 : 1)) release();
-      for (int b = 0; b < kBoxes; ++b) {
-        const int bx = odd ? b : kBoxes - 1 - b;
+      if (t.nkb == 0) {                                    // an expert without tokens: a zero gradient
         uint32_t w[32];
-        if (has) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) w[k] = 0u;
+        for (int bx = 0; bx < kBoxes; ++bx) store_box(w, rows, y_row, t.n0 + 128 * h + kBoxCols * bx, false);
+        continue;
+      }
+      const bool cut = kMode == Fp8GemmArgs::kDense && !kBf16Out && i >= p.cut0;
+      uint32_t* flag = p.flags + (static_cast<int64_t>(pair) * 2 + rank) * Cfg::kEpiWarps + (warp - Cfg::kFirstEpiWarp);
+      const int visit = visit_length<kBf16Out>(t.nkb);
+      for (int lo = 0; lo < t.nkb; lo += visit) {
+        uint32_t okw = 1;
+        if (lane == 0) {
+          okw = mbar_wait_backoff(acc_full, static_cast<uint32_t>(done) & 1u, p.status) ? 1u : 0u;
+          if (!kBf16Out) {
+            if (lo > 0) bulk_wait_group_all();             // this tile's earlier visit is in memory
+            // ... and so is the part below
+            else if (cut && t.part > 0 && okw != 0) okw = flag_take(flag - 2 * Cfg::kEpiWarps, p.status) ? 1u : 0u;
+          }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, okw, 0) != 0u;
+        if (!ok) break;
+        tc_fence_after();
+        const bool odd = (done & 1) != 0;
+        const uint32_t t_row = tmem + (static_cast<uint32_t>(32 * q) << 16) +
+                               static_cast<uint32_t>(Cfg::kAccStep * (odd ? 1 : 0) + 128 * h);
+        // The columns shared with the next visit come out first: the last 32 of
+        // an accumulator at column 0 (half 1), the first 32 of one at 224 (half
+        // 0).  Every warp arrives once a visit, the visit before being done
+        // with: then the next MMAs may write.
+        bool owe = true;
+        auto release = [&]() {
+          if (owe) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty_lead);
+            owe = false;
+          }
+        };
+        if (h != (odd ? 0 : 1)) release();
+        for (int b = 0; b < kBoxes; ++b) {
+          const int bx = odd ? b : kBoxes - 1 - b;
+          uint32_t w[32];
           if (kBf16Out) {
             // 32 columns as 16 bf16 pairs
             auto load_pack = [&](int half) {
@@ -440,36 +566,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
             tmem_ld_wait();
             release();
           }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) w[k] = 0u;
+          store_box(w, rows, y_row, t.n0 + 128 * h + kBoxCols * bx, lo > 0 || t.part > 0);
         }
-        const int64_t col = t.n0 + 128 * h + kBoxCols * bx;
-        if (rows <= 0 || col >= p.N) continue;             // the whole warp
-        if (kMode == Fp8GemmArgs::kRows && rows < 32) {
-          // the last rows of a segment: the rows behind them are not written
-          if (lane < rows) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.Y) + ((y_row + lane) * p.N + col) * kElem);
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              if (col + u * (16 / kElem) < p.N) dst[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-          }
-          continue;
-        }
-        if (lane == 0) bulk_wait_group_read<0>();          // the box's previous store has read it
-        __syncwarp();
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          *reinterpret_cast<uint4*>(box + lane * 128 + ((u ^ (lane & 7)) * 16)) =
-              make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&map_y, box, static_cast<int32_t>(col), static_cast<int32_t>(y_row));   // clipped at Y's edges
-          bulk_commit_group();
-        }
+        ++done;
       }
-      if (has) ++done;
+      if (cut && ok && t.part + 1 < p.parts && lane == 0) {
+        bulk_wait_group_all();
+        flag_set(flag);
+      }
     }
     if (lane == 0) bulk_wait_group_all();
   }
@@ -533,13 +637,30 @@ static cudaError_t gemm_t(const Fp8GemmArgs& a, cudaStream_t s) {
   p.a_oob = static_cast<int>(blocks128(a.a_rows) * 128);
   if (a.table) p.t = *a.table;
   p.Y = a.Y;
+  p.flags = a.flags;
   p.status = a.status;
   auto kern = fp8_gemm_kernel<kMode, kBf16Out>;
   const void* fn = reinterpret_cast<const void*>(kern);
   cudaError_t e = set_max_dynamic_smem(fn, Cfg::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int most = resident_pairs(fn);
-  const int pairs = tiles < most ? static_cast<int>(tiles) : most;
+  // one pair per two SMs that can hold pairs at once
+  int most = resident_pairs(fn);
+  if (most > kFp8MaxPairs) most = kFp8MaxPairs;
+  p.cut0 = 0x7FFFFFFF;
+  p.parts = 1;
+  if (kMode == Fp8GemmArgs::kDense && !kBf16Out && tiles % most != 0) {
+    // the last round's tiles: as many parts as there are pairs for, of at least
+    // kMinPart blocks, at most 4 (each waits for the one below)
+    const int rem = p.num_tiles % most;
+    int parts = most / rem < 4 ? most / rem : 4;
+    if (parts > p.nkb / kMinPart) parts = p.nkb / kMinPart;
+    if (parts > 1) {
+      p.cut0 = p.num_tiles - rem;
+      p.parts = parts;
+      p.num_tiles += rem * (parts - 1);
+    }
+  }
+  const int pairs = p.num_tiles < most ? p.num_tiles : most;
   return launch_ex(kern, dim3(2 * pairs), dim3(Cfg::kThreads), Cfg::kSmemBytes, s, true, ma, mb, msa, msb, my, p);
 }
 

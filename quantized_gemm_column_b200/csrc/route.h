@@ -96,6 +96,10 @@ cudaError_t launch_fp8_quant_weight(const void* W, avr_dtype wt, int E, int64_t 
                                     cudaStream_t s);
 
 // ---------------- 8-bit product (fp8_gemm.cu) ----------------
+// CTA pairs of a product; each has 16 flags in the workspace's tickets, zero between calls
+constexpr int kFp8MaxPairs = 128;
+static_assert(kFp8MaxPairs * 16 <= kMaxColTiles, "flags in the tickets");
+
 struct Fp8GemmArgs {
   const uint8_t* a_codes;      // [a_rows, K]
   const uint8_t* a_scales;
@@ -106,6 +110,7 @@ struct Fp8GemmArgs {
   void* Y;                     // [y_rows, N]
   int64_t y_rows;
   avr_dtype yt;
+  uint32_t* flags;
   uint32_t* status;
   // one product; the row tiles of the experts' buffer, B = the experts stacked;
   // or one product per expert along its tokens, Y = the experts stacked

@@ -168,6 +168,31 @@ def test_gemm_matches_fp64(api, M, N, K, yt):
     _check_product(Y, R.tensor_value(a), R.tensor_value(b), K)
 
 
+@pytest.mark.parametrize("M,N,K", [(260, 528, 20000), (1024, 1040, 6160), (16, 16, 12304), (300, 5136, 1600),
+                                   (2570, 4352, 3200)])
+def test_gemm_long_sums(api, M, N, K):
+    """Contractions summed in several visits, and tiles cut among pairs; the
+    same call twice gives the same bits, and leaves the workspace as it found it."""
+    a, b, ws = api.FP8Tensor(M, K), api.FP8Tensor(N, K), api.fp8_workspace(max(M, N), K, 16)
+    rng = torch.Generator(device="cuda").manual_seed(K)
+    for t in (a, b):
+        x = torch.randn(t.rows, K, generator=rng, device="cuda") + 0.5     # a mean: the sums grow with K
+        api.fp8_quant(x, t, ws)
+    Y, Z = torch.full((M, N), 7.0, device="cuda"), torch.full((M, N), 9.0, device="cuda")
+    ws[256:256 + 16384].zero_()
+    api.fp8_gemm(a, b, Y, ws)
+    api.fp8_gemm(a, b, Z, ws)
+    assert api.averis_check_status(ws) == 0 and not ws[:256 + 16384].any()
+    assert torch.equal(Y, Z)
+    A, B = (torch.from_numpy(R.tensor_value(t)).cuda() for t in (a, b))
+    ref, mag = A @ B.t(), A.abs() @ B.abs().t()
+    tol = K * 2.0 ** -24 * mag + 2.0 ** -24 * ref.abs()
+    assert ((Y.double() - ref).abs() <= tol).all()
+    # the drift of a visit: 192 instructions of 32 products, each cutting off at most 2^-23 of a running sum that
+    # averages half the visit's; visits are added in rounded fp32
+    assert ((Y.double() - ref).norm() / ref.norm()).item() <= 192 * 2.0 ** -24
+
+
 def test_gemm_places_every_code_and_scale(api):
     """A = rows of a unit matrix picks B's elements one by one, each with the
     scales of its row and block: exact."""
@@ -268,6 +293,21 @@ def _experts(api, E, m, n, dt, ws, seed=0):
     f, d = api.FP8Tensor(E * n, m), api.FP8Tensor(E * m, n)
     api.fp8_moe_quant_weights(W.cuda(), f, d, ws)
     return [R.deq(W[e].double().numpy(), (128, 128)) for e in range(E)], f, d
+
+
+def test_experts_long_contraction(api):
+    """fp32 rows summed in two visits, whole and ragged 32-row boxes."""
+    counts, m, n = [40, 0, 300, 7], 6400, 256
+    X, off = _buffer(counts, m, "bf16", 1)
+    ws = api.fp8_moe_workspace(X.shape[0], m, n, 4)
+    w, f, _ = _experts(api, 4, m, n, "bf16", ws)
+    Y = torch.full((X.shape[0], n), 7.0, device="cuda")
+    api.fp8_moe_linear_fwd(X.cuda(), torch.tensor(counts, dtype=torch.int32, device="cuda"), f, Y, ws)
+    assert api.averis_check_status(ws) == 0
+    for e, (o, c) in enumerate(zip(off, counts)):
+        if c:
+            _check_product(Y[o:o + c], R.deq(X[o:o + c].double().numpy()), w[e].T, m)
+        assert (Y[o + c:o + -(-c // 128) * 128] == 7.0).all()
 
 
 @pytest.mark.parametrize("counts", COUNTS)
