@@ -82,15 +82,26 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return v > -INFINITY ? u : 0u;
 }
 
+__device__ __forceinline__ float key_value(uint32_t u) {
+  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
 // Each of the k steps takes the largest key of the warp and, among the lanes
-// that hold it, the lowest expert: two warp reductions.  A lane's own best is
-// kept as a key and a register index, searched again only after it was taken.
+// that hold it, the lowest expert.  What bounds this is the number of
+// instructions (the logits are 17 MB for 32768 tokens of 128 experts), so a
+// step is kept short: a lane sorts its keys once (descending, the lower expert
+// first among equal ones; for up to 8, beyond that it searches), its best is
+// always the first, and the lane that holds the step's maximum notes its
+// expert in shared memory and moves up by one.  Lanes that tie, which is rare,
+// settle it by a second reduction.
 template <bool kBf16, int NV>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const void* logits, int64_t T, int E, int k, int norm,
                                                                  int32_t* ids, float* weights, uint32_t* status) {
+  __shared__ int32_t s_slot[kRouteWarps][kMaxSlots];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int lane = threadIdx.x & 31;
+  int32_t* slot = s_slot[threadIdx.x >> 5];
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (t >= T) return;
   float v[NV];
@@ -100,6 +111,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const void* log
   for (int i = 0; i < NV; ++i) {
     const int e = lane + 32 * i;
     v[i] = e < E ? load1<kBf16>(logits, t * E + e) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
     bad |= !(v[i] < INFINITY);
     key[i] = order_key(v[i]);
   }
@@ -111,46 +125,78 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const void* log
     }
     return;
   }
-  int my_id = -1;                     // lane j holds slot j
-  float my_v = -INFINITY, top = -INFINITY;
-  for (int j = 0; j < k; ++j) {
-    uint32_t best = key[0];
-    int at = 0;
-    float bv = v[0];
+  constexpr bool kSort = NV <= 8;
+  uint32_t order = 0x76543210u;       // kSort: which of the lane's experts the keys are, four bits each
+  if (kSort) {
+    // odd-even transposition: neighbours swap only when strictly out of order, so equal keys keep theirs
+    uint32_t at[NV];
 #pragma unroll
-    for (int i = 1; i < NV; ++i) {
-      if (key[i] > best) {            // strictly: the lower expert of equal ones
-        best = key[i];
-        at = i;
-        bv = v[i];
+    for (int i = 0; i < NV; ++i) at[i] = i;
+#pragma unroll
+    for (int r = 0; r < NV; ++r) {
+#pragma unroll
+      for (int i = r & 1; i + 1 < NV; i += 2) {
+        const bool swap = key[i] < key[i + 1];
+        const uint32_t x = swap ? key[i + 1] : key[i], y = swap ? key[i] : key[i + 1];
+        const uint32_t ax = swap ? at[i + 1] : at[i], ay = swap ? at[i] : at[i + 1];
+        key[i] = x;
+        key[i + 1] = y;
+        at[i] = ax;
+        at[i + 1] = ay;
+      }
+    }
+    order = at[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) order |= at[i] << (4 * i);
+  }
+  uint32_t my_key = 0u;               // lane j holds slot j
+  int taken = 0;
+  for (; taken < k; ++taken) {
+    uint32_t best = key[0];
+    uint32_t best_at = kSort ? order & 15u : 0u;
+    if (!kSort) {
+#pragma unroll
+      for (int i = 1; i < NV; ++i) {
+        if (key[i] > best) {          // strictly: the lower expert of equal ones
+          best = key[i];
+          best_at = i;
+        }
       }
     }
     const uint32_t m = __reduce_max_sync(kFull, best);
     if (m == 0u) break;               // only -inf left
-    const uint32_t e = __reduce_min_sync(kFull, best == m ? static_cast<uint32_t>(lane + 32 * at) : 0xFFFFFFFFu);
-    const float ev = __shfl_sync(kFull, bv, static_cast<int>(e & 31u));
-    if (j == 0) top = ev;
-    if (lane == j) {
-      my_id = static_cast<int>(e);
-      my_v = ev;
-    }
+    const uint32_t e = lane + 32u * best_at;
+    bool mine = best == m;
+    const uint32_t tie = __ballot_sync(kFull, mine);
+    if (tie & (tie - 1u)) mine = e == __reduce_min_sync(kFull, mine ? e : 0xFFFFFFFFu);
+    if (lane == taken) my_key = m;
+    if (mine) {
+      slot[taken] = static_cast<int32_t>(e);
+      if (kSort) {
+        order >>= 4;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (static_cast<uint32_t>(lane + 32 * i) == e) key[i] = 0u;
+        for (int i = 0; i + 1 < NV; ++i) key[i] = key[i + 1];
+        key[NV - 1] = 0u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (i == static_cast<int>(best_at)) key[i] = 0u;
+      }
+    }
   }
-  const float mine = my_id >= 0 ? expf(my_v - top) : 0.0f;
+  __syncwarp();
+  const float top = key_value(__shfl_sync(kFull, my_key, 0));
+  const float mine = lane < taken ? expf(key_value(my_key) - top) : 0.0f;
   float den = mine;
-  if (!norm) {
+  if (!norm && taken > 0) {
     den = 0.0f;
-    if (top > -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) den += expf(v[i] - top);
-    }
+    for (int i = 0; i < NV; ++i) den += expf(v[i] - top);
   }
   den = warp_sum(den);
   if (lane < k) {
-    ids[t * k + lane] = my_id;
-    weights[t * k + lane] = my_id >= 0 ? mine / den : 0.0f;
+    ids[t * k + lane] = lane < taken ? slot[lane] : -1;
+    weights[t * k + lane] = lane < taken ? mine / den : 0.0f;
   }
 }
 
@@ -167,6 +213,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   float* row = s_row[threadIdx.x >> 5];
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (t >= T) return;
+  float v[NV];
+  if (!norm) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane + 32 * i;
+      v[i] = e < E ? load1<kBf16>(logits, t * E + e) : -INFINITY;
+    }
+  }
   int id = -1;
   float w = 0.0f, dw = 0.0f;
   if (lane < k) {
@@ -184,10 +238,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 #pragma unroll
   for (int i = 0; i < NV; ++i) row[lane + 32 * i] = 0.0f;
   __syncwarp();
-  // one slot after another: a row that names an expert twice adds in slot order
-  for (int j = 0; j < k; ++j) {
-    if (lane == j && id >= 0) row[id] += norm ? w * (dw - s) : w * dw;
-    __syncwarp();
+  // every slot leaves its number at its expert; a slot that finds another's
+  // there shares the expert with it (a row that names one twice)
+  const float g = norm ? w * (dw - s) : w * dw;
+  if (id >= 0) row[id] = __int_as_float(lane);
+  __syncwarp();
+  const bool shared = id >= 0 && __float_as_int(row[id]) != lane;
+  const bool any_shared = __any_sync(kFull, shared);
+  if (id >= 0) row[id] = any_shared ? 0.0f : g;
+  __syncwarp();
+  if (any_shared) {                   // then one slot after another
+    for (int j = 0; j < k; ++j) {
+      if (lane == j && id >= 0) row[id] += g;
+      __syncwarp();
+    }
   }
   if (norm) {
 #pragma unroll
@@ -195,13 +259,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
       if (lane + 32 * i < E) store1<kBf16>(dlogits, t * E + lane + 32 * i, row[lane + 32 * i]);
     return;
   }
-  float v[NV], top = -INFINITY, den = 0.0f;
+  float top = -INFINITY, den = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
-    v[i] = e < E ? load1<kBf16>(logits, t * E + e) : -INFINITY;
-    top = fmaxf(top, v[i]);
-  }
+  for (int i = 0; i < NV; ++i) top = fmaxf(top, v[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
 #pragma unroll
@@ -420,7 +480,7 @@ cudaError_t launch_sort(const int32_t* ids, int64_t slots, int E, int64_t l_cap,
 // row of X, Y or dY is moved once whatever k is, and the buffer's rows once
 // each.  A warp takes (token, strip of 32 lanes x kU 16-byte vectors).
 // ---------------------------------------------------------------------------
-constexpr int kPermThreads = 256;
+constexpr int kPermThreads = 128;
 
 // the buffer row of slot (t, j), -1 for none
 __device__ __forceinline__ int64_t slot_row(const PermuteArgs& a, int64_t t, int j) {
@@ -459,10 +519,15 @@ __global__ void __launch_bounds__(kPermThreads) dispatch_kernel(const PermuteArg
   }
 }
 
-constexpr int kCombU = 2;
+// A strip is 2 KB of each of the token's rows.  Longer pieces of a row at a
+// time are what HBM wants: 512-byte strips with more slots' loads in flight
+// took 66-73 us where these take 52 (8192 tokens, 8 slots, 2048 bf16).  The
+// token's rows and weights are held by lanes, so that no load of a vector
+// waits for one of an index.
+constexpr int kCombU = 4;
 
 template <bool kBf16, bool kWeighted>
-__global__ void __launch_bounds__(kPermThreads) combine_kernel(const PermuteArgs a, int64_t V, int strips) {
+__global__ void __launch_bounds__(kPermThreads, 4) combine_kernel(const PermuteArgs a, int64_t V, int strips) {
   constexpr int N = Vec<kBf16>::kN;
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
@@ -474,12 +539,14 @@ __global__ void __launch_bounds__(kPermThreads) combine_kernel(const PermuteArgs
        task < a.T * strips; task += warps) {
     const int64_t t = task / strips;
     const int64_t v0 = (task % strips) * (32 * kCombU) + lane;
+    const int row = lane < a.k ? static_cast<int>(slot_row(a, t, lane)) : -1;
+    const float weight = kWeighted && row >= 0 ? __ldg(a.weights + t * a.k + lane) : 0.0f;
     float acc[kCombU][N] = {};
-#pragma unroll 4
+#pragma unroll 2
     for (int j = 0; j < a.k; ++j) {
-      const int64_t r = slot_row(a, t, j);
+      const int r = __shfl_sync(kFull, row, j);
+      const float w = __shfl_sync(kFull, weight, j);
       if (r < 0) continue;
-      const float w = kWeighted ? __ldg(a.weights + t * a.k + j) : 1.0f;
 #pragma unroll
       for (int u = 0; u < kCombU; ++u) {
         if (v0 + 32 * u < V) {
@@ -497,8 +564,9 @@ __global__ void __launch_bounds__(kPermThreads) combine_kernel(const PermuteArgs
 }
 
 // One CTA per token: dY's row stays in L1 over the slots, and the dot products
-// of all slots are summed in the same order whatever the grid.
-constexpr int kBwdThreads = 128;
+// of all slots are summed in the same order whatever the grid.  The block has
+// as many threads as make whole passes over the row's vectors, 128 at most.
+constexpr int kBwdThreads = 128, kBwdJ = 2;
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kBwdThreads) combine_bwd_kernel(const PermuteArgs a, int64_t V) {
@@ -511,31 +579,48 @@ __global__ void __launch_bounds__(kBwdThreads) combine_bwd_kernel(const PermuteA
   const uint4* yp = static_cast<const uint4*>(a.yp);
   uint4* dst = static_cast<uint4*>(a.dst);
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t r = slot_row(a, t, j);
-      float dot = 0.0f;
-      if (r >= 0) {
-        const float w = __ldg(a.weights + t * a.k + j);
-        for (int64_t v = threadIdx.x; v < V; v += kBwdThreads) {
-          float d[N], y[N], o[N];
-          unpack<kBf16>(__ldg(dy + t * V + v), d);
-          unpack<kBf16>(__ldg(yp + r * V + v), y);
+    const int row = lane < a.k ? static_cast<int>(slot_row(a, t, lane)) : -1;
+    const float weight = row >= 0 ? __ldg(a.weights + t * a.k + lane) : 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += kBwdJ) {
+      int r[kBwdJ];
+      float w[kBwdJ], dot[kBwdJ];
+#pragma unroll
+      for (int j = 0; j < kBwdJ; ++j) {
+        r[j] = __shfl_sync(kFull, row, (j0 + j) & 31);
+        w[j] = __shfl_sync(kFull, weight, (j0 + j) & 31);
+        if (j0 + j >= a.k) r[j] = -1;
+        dot[j] = 0.0f;
+      }
+      for (int64_t v = threadIdx.x; v < V; v += blockDim.x) {
+        uint4 q[kBwdJ];
+        float d[N];
+#pragma unroll
+        for (int j = 0; j < kBwdJ; ++j)
+          if (r[j] >= 0) q[j] = __ldg(yp + r[j] * V + v);
+        unpack<kBf16>(__ldg(dy + t * V + v), d);
+#pragma unroll
+        for (int j = 0; j < kBwdJ; ++j) {
+          if (r[j] < 0) continue;
+          float y[N], o[N];
+          unpack<kBf16>(q[j], y);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            dot = fmaf(d[i], y[i], dot);
-            o[i] = w * d[i];
+            dot[j] = fmaf(d[i], y[i], dot[j]);
+            o[i] = w[j] * d[i];
           }
-          dst[r * V + v] = pack<kBf16>(o);
+          dst[r[j] * V + v] = pack<kBf16>(o);
         }
       }
-      dot = warp_sum(dot);
-      if (lane == 0) s_dot[warp][j] = dot;
+#pragma unroll
+      for (int j = 0; j < kBwdJ; ++j) {
+        dot[j] = warp_sum(dot[j]);
+        if (lane == 0 && j0 + j < a.k) s_dot[warp][j0 + j] = dot[j];
+      }
     }
     __syncthreads();
     if (threadIdx.x < a.k) {
       float sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kBwdThreads / 32; ++w) sum += s_dot[w][threadIdx.x];
+      for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) sum += s_dot[w][threadIdx.x];
       a.dweights[t * a.k + threadIdx.x] = sum;
     }
     __syncthreads();
@@ -572,10 +657,11 @@ cudaError_t launch_combine(const PermuteArgs& a, cudaStream_t s) {
 template <bool kBf16>
 static cudaError_t combine_bwd_t(const PermuteArgs& a, cudaStream_t s) {
   auto kern = combine_bwd_kernel<kBf16>;
+  const int64_t V = a.H / Vec<kBf16>::kN, passes = (V + kBwdThreads - 1) / kBwdThreads;
+  const int threads = static_cast<int>(((V + passes - 1) / passes + 31) / 32 * 32);
   const int64_t most = static_cast<int64_t>(sm_count()) *
-                       blocks_per_sm(reinterpret_cast<const void*>(kern), kBwdThreads, 0) * 4;
-  return launch_ex(kern, dim3(static_cast<unsigned>(a.T < most ? a.T : most)), dim3(kBwdThreads), 0, s, true, a,
-                   a.H / Vec<kBf16>::kN);
+                       blocks_per_sm(reinterpret_cast<const void*>(kern), threads, 0) * 4;
+  return launch_ex(kern, dim3(static_cast<unsigned>(a.T < most ? a.T : most)), dim3(threads), 0, s, true, a, V);
 }
 
 cudaError_t launch_combine_bwd(const PermuteArgs& a, cudaStream_t s) {
