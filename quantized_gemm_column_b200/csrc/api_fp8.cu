@@ -28,7 +28,7 @@ avr_status check_fp8(const avr_fp8* t, int64_t rows, int64_t K) {
 // the two token-axis operands of the weight gradient, and before them the
 // experts' tables (l_cap rows)
 struct Fp8Layout {
-  size_t seg = 0, block_expert = 0, tiles = 0, totals = 0;
+  size_t seg = 0, block_expert = 0, tiles = 0, order = 0, totals = 0;
   size_t q_codes = 0, q_scales = 0;                                        // [l, max(m, n)]
   size_t xt_codes = 0, xt_scales = 0, dt_codes = 0, dt_scales = 0;         // [m, L], [n, L]
   size_t tables = 0, total = 0;                                            // bytes up to the operands; of all
@@ -42,6 +42,7 @@ Fp8Layout fp8_layout(int64_t l, int64_t m, int64_t n, int E) {
     w.seg = off;          off = align256(off + static_cast<size_t>(E) * sizeof(Fp8Seg));
     w.block_expert = off; off = align256(off + blocks * sizeof(int32_t));
     w.tiles = off;        off = align256(off + blocks * sizeof(Fp8Tile));
+    w.order = off;        off = align256(off + static_cast<size_t>(E) * sizeof(int32_t));
     w.totals = off;       off += 256;
   }
   w.tables = off;
@@ -65,7 +66,7 @@ T* at(void* ws, size_t off) {
 
 Fp8Table table_at(void* ws, const Fp8Layout& w) {
   return Fp8Table{at<Fp8Seg>(ws, w.seg), at<int32_t>(ws, w.block_expert), at<Fp8Tile>(ws, w.tiles),
-                  at<int32_t>(ws, w.totals)};
+                  at<int32_t>(ws, w.order), at<int32_t>(ws, w.totals)};
 }
 
 Fp8QuantArgs quant_args(const void* X, avr_dtype xt, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,

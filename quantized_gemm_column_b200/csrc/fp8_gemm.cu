@@ -148,7 +148,12 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int i, int rank) {
     t.nkb = p.nkb;
     t.y_row = v.x + rank * 128;
   } else {
-    const int per = p.tiles_m * p.tiles_n, e = i / per, r = i - e * per;
+    // The experts come with the most tokens first and every other round of
+    // tiles goes to the pairs backwards, so that the pairs' sums of blocks come
+    // out alike (in the experts' own order a few large ones decide the time).
+    const int per = p.tiles_m * p.tiles_n, pairs = static_cast<int>(gridDim.x) / 2, round = i / pairs;
+    if ((round & 1) != 0 && (round + 1) * pairs <= p.num_tiles) i = (2 * round + 1) * pairs - 1 - i;
+    const int r = i % per, e = __ldcg(p.t.order + i / per);
     const int2 sg = __ldcg(reinterpret_cast<const int2*>(p.t.seg) + e);
     const int m0 = r / p.tiles_n * 256 + rank * 128;
     t.n0 = r % p.tiles_n * 256;

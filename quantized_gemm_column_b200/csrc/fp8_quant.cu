@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kTableThreads) fp8_table_kernel(const int32_t*
   const bool fits = !any_bad && static_cast<int64_t>(all & kLow) <= n_blocks;
   const int32_t blocks = fits ? static_cast<int32_t>(all & kLow) : 0;
   const int32_t tiles = fits ? static_cast<int32_t>(all >> kShift) : 0;
+  if (tid < E) s_rows[tid] = n;
   if (tid < E && fits) {
-    s_rows[tid] = n;
     s_blk[tid] = static_cast<int32_t>(x & kLow);
     s_tile[tid] = static_cast<int32_t>(x >> kShift);
     t.seg[tid] = Fp8Seg{static_cast<int32_t>(128 * ((x & kLow) - blk)), n};
@@ -139,6 +139,11 @@ __global__ void __launch_bounds__(kTableThreads) fp8_table_kernel(const int32_t*
     if (!fits) raise_status(status, AVR_ERR_INVALID_ARG);
   }
   __syncthreads();
+  if (tid < E && fits) {
+    int rank = 0;
+    for (int e = 0; e < E; ++e) rank += s_rows[e] > n || (s_rows[e] == n && e < tid) ? 1 : 0;
+    t.order[rank] = tid;
+  }
   // the first expert whose end lies past i
   auto find = [&](const int32_t* end, int32_t i) {
     int lo = 0, hi = E - 1;

@@ -70,6 +70,7 @@ struct Fp8Table {
   Fp8Seg* seg;              // [E]
   int32_t* block_expert;    // [l_cap / 128]
   Fp8Tile* tiles;           // [l_cap / 128]
+  int32_t* order;           // [E] experts, the ones with the most tokens first
   int32_t* totals;          // {tiles, 1 when the segments fit}
 };
 cudaError_t launch_fp8_table(const int32_t* counts, int E, int64_t l_cap, const Fp8Table& t, uint32_t* status,
