@@ -506,7 +506,8 @@ avr_status fp8_gemm(const avr_fp8* a, const avr_fp8* b, void* Y, avr_dtype yt, v
                     avr_stream stream);
 
 /* Y [l, n] = Q(X) Q(W), dX [l, m] = Q(D) Q(W)^T, dW [m, n] = Q(X^T) Q(D^T)^T
- * (0 when l = 0).  Launch 2, 2 and 3 kernels. */
+ * (0 when l = 0).  Launch 2, 2 and 3 kernels; the first two 1 for a few
+ * tokens, whose sums then have another order. */
 avr_status fp8_linear_fwd(const void* X, avr_dtype xt, int64_t l, int64_t m, int64_t n, const avr_fp8* w_fwd, void* Y,
                           avr_dtype yt, void* ws, size_t ws_bytes, avr_stream stream);
 avr_status fp8_linear_dgrad(const void* D, avr_dtype dt, int64_t l, int64_t m, int64_t n, const avr_fp8* w_dgrad,

@@ -114,6 +114,8 @@ avr_status linear(const void* X, avr_dtype xt, int64_t l, int64_t K, int64_t N, 
   const Fp8Layout lay = fp8_layout(l, m, n, 0);
   AVR_TRY(check_ws(ws, ws_bytes, lay.total));
   AVR_TRY(device_ok());
+  if (fp8_skinny_applies(l, K, N))
+    return cuda_status(launch_fp8_skinny({X, xt, l, K, N, w->codes, w->scales, Y, yt, status_of(ws)}, stream));
   uint8_t *codes = at<uint8_t>(ws, lay.q_codes), *scales = at<uint8_t>(ws, lay.q_scales);
   AVR_TRY(cuda_status(launch_fp8_quant(quant_args(X, xt, l, K, codes, scales, ws), stream)));
   return cuda_status(

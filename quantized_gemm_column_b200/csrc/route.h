@@ -121,4 +121,19 @@ struct Fp8GemmArgs {
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t s);
 
+// ---------------- 8-bit linear layer of a few tokens (fp8_skinny.cu) ----------------
+// Y [l, N] = Q(X) w^T, w [N, K]
+struct Fp8SkinnyArgs {
+  const void* X;
+  avr_dtype xt;
+  int64_t l, K, N;
+  const uint8_t* w_codes;
+  const uint8_t* w_scales;
+  void* Y;
+  avr_dtype yt;
+  uint32_t* status;
+};
+bool fp8_skinny_applies(int64_t l, int64_t K, int64_t N);
+cudaError_t launch_fp8_skinny(const Fp8SkinnyArgs& a, cudaStream_t s);
+
 }  // namespace avr

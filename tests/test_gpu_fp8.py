@@ -215,7 +215,8 @@ def _weights(api, m, n, dt, seed, ws):
     return R.deq(W.double().numpy(), (128, 128)), f, d
 
 
-@pytest.mark.parametrize("l,m,n", [(1, 16, 16), (1, 1024, 640), (2, 144, 272), (17, 256, 2064), (129, 1040, 400),
+@pytest.mark.parametrize("l,m,n", [(1, 16, 16), (1, 1024, 640), (2, 144, 272), (3, 528, 6000), (5, 272, 1040),
+                                   (8, 6144, 64), (8, 6160, 48), (9, 640, 128), (17, 256, 2064), (129, 1040, 400),
                                    (1000, 272, 528)])
 @pytest.mark.parametrize("dt,ot", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16")])
 def test_linear_forward_and_gradients(api, l, m, n, dt, ot):
@@ -232,6 +233,35 @@ def test_linear_forward_and_gradients(api, l, m, n, dt, ot):
     _check_product(Y, R.deq(x), w.T, m)
     _check_product(dX, R.deq(dd), w, n)
     _check_product(dW, R.deq(x.T.copy()), R.deq(dd.T.copy()), l)
+
+
+@pytest.mark.parametrize("l", [1, 2, 4, 8, 16])
+def test_linear_extreme_scales(api, l):
+    """Blocks whose scales' product leaves fp32's exponent range in parts only,
+    and results near its ends: few tokens and many go different ways."""
+    m, n = 256, 32
+    ws = api.fp8_workspace(l, m, n)
+    X, W = torch.ones(l, m), torch.ones(m, n)
+    X[:, :128] *= 2.0 ** 100
+    W[:128] *= 2.0 ** -100
+    X[:, 128:] *= 2.0 ** -126
+    W[128:] *= 2.0 ** 118
+    f = api.FP8Tensor(n, m)
+    api.fp8_quant_weight(W.cuda(), f, None, ws)
+    Y = torch.empty(l, n, device="cuda")
+    api.fp8_linear_fwd(X.cuda(), f, Y, ws)
+    assert api.averis_check_status(ws) == 0
+    assert (Y == 128.5).all()
+
+
+def test_linear_few_tokens_latch_non_finite(api):
+    ws, f = api.fp8_workspace(3, 528, 64), api.FP8Tensor(64, 528)
+    api.fp8_quant_weight(_x(528, 64, "f32").cuda(), f, None, ws)
+    X, Y = _x(3, 528, "f32"), torch.empty(3, 64, device="cuda")
+    X[2, 527] = float("nan")
+    api.fp8_linear_fwd(X.cuda(), f, Y, ws)
+    assert api.averis_check_status(ws) == api.AVR_ERR_NONFINITE
+    assert torch.isfinite(Y[:2]).all()
 
 
 def test_linear_no_tokens(api):
