@@ -533,7 +533,7 @@ avr_status fp8_moe_dispatch(const void* X, avr_dtype xt, int64_t T, int k, int64
                             const avr_fp8* xq, void* ws, size_t ws_bytes, avr_stream stream);
 
 /* Y[r] = xq[r] W_e^T for the rows r of every expert e, w = the experts' [N, K]
- * stacked (rows = E N).  Launches 2 kernels. */
+ * stacked (rows = E N).  Launches 1 kernel. */
 avr_status fp8_moe_gemm(const avr_fp8* xq, const int32_t* counts, int E, const avr_fp8* w, void* Y, avr_dtype yt,
                         void* ws, size_t ws_bytes, avr_stream stream);
 

@@ -28,10 +28,10 @@ avr_status check_fp8(const avr_fp8* t, int64_t rows, int64_t K) {
 // the two token-axis operands of the weight gradient, and before them the
 // experts' tables (l_cap rows)
 struct Fp8Layout {
-  size_t seg = 0, block_expert = 0, tiles = 0, order = 0, totals = 0;
+  size_t seg = 0, block_expert = 0, order = 0, fits = 0;
   size_t q_codes = 0, q_scales = 0;                                        // [l, max(m, n)]
   size_t xt_codes = 0, xt_scales = 0, dt_codes = 0, dt_scales = 0;         // [m, L], [n, L]
-  size_t tables = 0, total = 0;                                            // bytes up to the operands; of all
+  size_t total = 0;
 };
 
 Fp8Layout fp8_layout(int64_t l, int64_t m, int64_t n, int E) {
@@ -41,11 +41,9 @@ Fp8Layout fp8_layout(int64_t l, int64_t m, int64_t n, int E) {
     const size_t blocks = static_cast<size_t>(l / 128);
     w.seg = off;          off = align256(off + static_cast<size_t>(E) * sizeof(Fp8Seg));
     w.block_expert = off; off = align256(off + blocks * sizeof(int32_t));
-    w.tiles = off;        off = align256(off + blocks * sizeof(Fp8Tile));
     w.order = off;        off = align256(off + static_cast<size_t>(E) * sizeof(int32_t));
-    w.totals = off;       off += 256;
+    w.fits = off;         off += 256;
   }
-  w.tables = off;
   const int64_t K = m > n ? m : n, L = blocks128(l) * 128;
   w.q_codes = off;
   w.q_scales = align256(w.q_codes + static_cast<size_t>(l) * static_cast<size_t>(K));
@@ -65,8 +63,8 @@ T* at(void* ws, size_t off) {
 }
 
 Fp8Table table_at(void* ws, const Fp8Layout& w) {
-  return Fp8Table{at<Fp8Seg>(ws, w.seg), at<int32_t>(ws, w.block_expert), at<Fp8Tile>(ws, w.tiles),
-                  at<int32_t>(ws, w.order), at<int32_t>(ws, w.totals)};
+  return Fp8Table{at<Fp8Seg>(ws, w.seg), at<int32_t>(ws, w.block_expert), at<int32_t>(ws, w.order),
+                  at<int32_t>(ws, w.fits)};
 }
 
 Fp8QuantArgs quant_args(const void* X, avr_dtype xt, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,
@@ -127,14 +125,14 @@ bool moe_sizes_ok(int64_t l_cap, int E, int64_t m, int64_t n) {
          rows_ok(E * m) && rows_ok(E * n);
 }
 
-// Y rows of every expert from xq; `table` is in place
+// Y rows of every expert from xq
 avr_status moe_product(const uint8_t* codes, const uint8_t* scales, int64_t l_cap, int64_t K, int E,
-                       const avr_fp8* w, int64_t N, const Fp8Table& table, void* Y, avr_dtype yt, void* ws,
+                       const avr_fp8* w, int64_t N, const int32_t* counts, void* Y, avr_dtype yt, void* ws,
                        cudaStream_t s) {
   Fp8GemmArgs g = gemm_args(codes, scales, l_cap, w->codes, w->scales, E * N, K, l_cap, N, Y, l_cap, yt, ws);
   g.mode = Fp8GemmArgs::kRows;
   g.E = E;
-  g.table = &table;
+  g.counts = counts;
   return cuda_status(launch_fp8_gemm(g, s));
 }
 
@@ -156,7 +154,7 @@ avr_status moe_linear(const void* X, avr_dtype xt, int64_t l_cap, const int32_t*
   Fp8QuantArgs q = quant_args(X, xt, l_cap, K, codes, scales, ws);
   q.table = &table;
   AVR_TRY(cuda_status(launch_fp8_quant(q, stream)));
-  return moe_product(codes, scales, l_cap, K, E, w, N, table, Y, yt, ws, stream);
+  return moe_product(codes, scales, l_cap, K, E, w, N, counts, Y, yt, ws, stream);
 }
 
 // what the calls on the experts' buffer check alike; `buf`s may be null only when they have no rows
@@ -423,13 +421,10 @@ avr_status fp8_moe_gemm(const avr_fp8* xq, const int32_t* counts, int E, const a
   if (l_cap > 0) AVR_TRY(check_fp8(xq, l_cap, K));
   AVR_TRY(check_fp8(w, E * N, K));
   if (!aligned16(Y) || !aligned4(counts)) return AVR_ERR_MISALIGNED;
-  const Fp8Layout lay = fp8_layout(l_cap, K, N, E);
-  AVR_TRY(check_ws(ws, ws_bytes, lay.tables));
+  AVR_TRY(check_ws(ws, ws_bytes, kScratch));
   AVR_TRY(device_ok());
-  const Fp8Table table = table_at(ws, lay);
-  AVR_TRY(cuda_status(launch_fp8_table(counts, E, l_cap, table, status_of(ws), stream)));
   if (l_cap == 0) return AVR_OK;
-  return moe_product(xq->codes, xq->scales, l_cap, K, E, w, N, table, Y, yt, ws, stream);
+  return moe_product(xq->codes, xq->scales, l_cap, K, E, w, N, counts, Y, yt, ws, stream);
 }
 
 avr_status fp8_moe_linear_fwd(const void* X, avr_dtype xt, int64_t l_cap, const int32_t* counts, int E, int64_t m,

@@ -79,7 +79,7 @@ struct Cfg {
   static constexpr int kSfbOffset = kSfaOffset + kSlots * kSfaBytes;
   static constexpr int kBarOffset = kSfbOffset + kSlots * kSfbBytes;
   static constexpr int kSmemBytes = kBarOffset + 256;
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+  static_assert(kSmemBytes + 3 * 4 * kMaxExperts + 256 <= 227 * 1024, "shared memory budget");
   // tensor memory: the accumulators at columns 0 and 224, then the scale slots
   static constexpr int kAccStep = 224;
   static constexpr int kSfaCol = kAccStep + kBN;                // 480
@@ -95,10 +95,12 @@ struct Cfg {
 struct Params {
   int64_t M, N;
   int tiles_m, tiles_n, nkb;      // kTokens: per expert, nkb unused
-  int num_tiles;                  // kRows: computed from the table's tile count
+  int num_tiles;                  // kRows: at most; the counts give the rest
   int cut0, parts;                // tiles from cut0 on are cut into parts (kDense, fp32; else past the end, 1)
   int a_oob;                      // a row coordinate past A: reads zeros
-  Fp8Table t;
+  int E;
+  const int32_t* counts;          // kRows: the experts' tokens, turned into row tiles by every CTA
+  Fp8Table t;                     // kTokens
   void* Y;
   uint32_t* flags;                // [pairs][2][8], zero between launches: a warp's share of a part is stored
   uint32_t* status;
@@ -114,8 +116,65 @@ struct Tile {
   int32_t part;                   // kDense: which part of the tile (0: all, or the first)
 };
 
+// kRows: the experts' buffer in shared memory
+struct Buffer {
+  int32_t rows[kMaxExperts];       // tokens
+  int32_t blk_end[kMaxExperts];    // 128-row blocks up to and with this expert
+  int32_t tile_end[kMaxExperts];   // 256-row tiles likewise
+  uint64_t warp[32];
+};
+
+// Fills it from the counts, by the whole CTA; the number of row tiles, 0 when
+// the segments do not fit l_cap rows.
+__device__ __forceinline__ int scan_counts(const int32_t* counts, int E, int64_t l_cap, Buffer* b, uint32_t* status) {
+  static_assert(2 * Cfg::kThreads >= kMaxExperts, "two experts a thread");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int32_t n[2];
+  uint64_t x[2];
+  bool bad = false;
+  // blocks in the low 35 bits of a word (1024 counts of at most 2^24 blocks),
+  // tiles above them: when the segments fit there are at most 2^24 tiles
+  constexpr int kShift = 35;
+  constexpr uint64_t kLow = (1ull << kShift) - 1;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    n[i] = 2 * tid + i < E ? __ldcg(counts + 2 * tid + i) : 0;
+    const bool out = n[i] < 0 || n[i] > l_cap;
+    bad |= out;
+    const uint64_t blk = out ? 0 : (static_cast<uint64_t>(n[i]) + 127) / 128;
+    x[i] = blk | (((blk + 1) / 2) << kShift);
+  }
+  uint64_t sum = x[0] + x[1];
+  const uint64_t own = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+    if (lane >= o) sum += y;
+  }
+  if (lane == 31) b->warp[warp] = sum;
+  const bool any_bad = __syncthreads_or(bad) != 0;
+  uint64_t before = sum - own, all = 0;
+  for (int w = 0; w < Cfg::kThreads / 32; ++w) {
+    before += w < warp ? b->warp[w] : 0;
+    all += b->warp[w];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    before += x[i];
+    if (2 * tid + i < E) {
+      b->rows[2 * tid + i] = n[i];
+      b->blk_end[2 * tid + i] = static_cast<int32_t>(before & kLow);
+      b->tile_end[2 * tid + i] = static_cast<int32_t>(before >> kShift);
+    }
+  }
+  const bool fits = !any_bad && static_cast<int64_t>(all & kLow) <= l_cap / 128;
+  if (!fits && blockIdx.x == 0 && tid == 0) raise_status(status, AVR_ERR_INVALID_ARG);
+  __syncthreads();
+  return fits ? static_cast<int>(all >> kShift) : 0;
+}
+
 template <int kMode>
-__device__ __forceinline__ Tile tile_at(const Params& p, int i, int rank) {
+__device__ __forceinline__ Tile tile_at(const Params& p, const Buffer* b, int i, int rank) {
   Tile t;
   t.part = 0;
   if (kMode == Fp8GemmArgs::kDense) {
@@ -139,14 +198,24 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int i, int rank) {
     t.y_row = m0;
     t.rows = static_cast<int32_t>(min64(128, p.M - m0));
   } else if (kMode == Fp8GemmArgs::kRows) {
-    const int4 v = __ldcg(reinterpret_cast<const int4*>(p.t.tiles) + i / p.tiles_n);   // row0, expert, rows
+    const int mt = i / p.tiles_n;
+    int lo = 0, hi = p.E - 1;                            // the first expert whose tiles end past mt
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (b->tile_end[mid] > mt)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    const int off = 256 * (mt - (lo > 0 ? b->tile_end[lo - 1] : 0));
+    const int row0 = 128 * (lo > 0 ? b->blk_end[lo - 1] : 0) + off + rank * 128;
     t.n0 = i % p.tiles_n * 256;
-    t.rows = min(128, v.z - rank * 128);
-    t.a_row = t.rows > 0 ? v.x + rank * 128 : p.a_oob;   // the other CTA's block may be another expert's
-    t.b_row0 = v.y * static_cast<int32_t>(p.N) + t.n0;
+    t.rows = min(128, b->rows[lo] - off - rank * 128);
+    t.a_row = t.rows > 0 ? row0 : p.a_oob;               // the other CTA's block may be another expert's
+    t.b_row0 = lo * static_cast<int32_t>(p.N) + t.n0;
     t.kb0 = 0;
     t.nkb = p.nkb;
-    t.y_row = v.x + rank * 128;
+    t.y_row = row0;
   } else {
     // The experts come with the most tokens first and every other round of
     // tiles goes to the pairs backwards, so that the pairs' sums of blocks come
@@ -302,8 +371,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
 
   const int pairs = static_cast<int>(gridDim.x) / 2, pair = static_cast<int>(blockIdx.x) / 2;
   int num_tiles = p.num_tiles;
-  if (kMode == Fp8GemmArgs::kRows) num_tiles = __ldcg(p.t.totals) * p.tiles_n;
-  if (kMode == Fp8GemmArgs::kTokens && __ldcg(p.t.totals + 1) == 0) num_tiles = 0;   // the counts did not fit
+  Buffer* buffer = reinterpret_cast<Buffer*>(smem_raw + Cfg::kSmemBytes);
+  if (kMode == Fp8GemmArgs::kRows) num_tiles = scan_counts(p.counts, p.E, p.M, buffer, p.status) * p.tiles_n;
+  if (kMode == Fp8GemmArgs::kTokens && __ldcg(p.t.fits) == 0) num_tiles = 0;   // the counts did not fit
   // both CTAs of a pair leave their loops together: a CTA whose shared memory
   // is misaligned has a misaligned partner (same launch), so neither works
   if (!aligned) num_tiles = 0;
@@ -317,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
       int it = 0;
       bool ok = true;
       for (int i = pair; i < num_tiles && ok; i += pairs) {
-        const Tile t = tile_at<kMode>(p, i, rank);
+        const Tile t = tile_at<kMode>(p, buffer, i, rank);
         for (int kb = t.kb0; kb < t.kb0 + t.nkb; ++kb, ++it) {
           if ((it & 1) != parity) continue;
           const int st = it % Cfg::kStages;
@@ -342,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
       int it = 0;
       bool ok = true;
       for (int i = pair; i < num_tiles && ok; i += pairs) {
-        const Tile t = tile_at<kMode>(p, i, rank);
+        const Tile t = tile_at<kMode>(p, buffer, i, rank);
         if (t.nkb == 0) continue;
         for (int c = t.kb0 >> 2; c <= (t.kb0 + t.nkb - 1) >> 2; ++c, ++it) {
           const int sl = it % Cfg::kSlots;
@@ -366,7 +436,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
       int it = 0;
       bool ok = true;
       for (int i = pair; i < num_tiles && ok; i += pairs) {
-        const Tile t = tile_at<kMode>(p, i, 0);
+        const Tile t = tile_at<kMode>(p, buffer, i, 0);
         if (t.nkb == 0) continue;
         for (int c = t.kb0 >> 2; c <= (t.kb0 + t.nkb - 1) >> 2; ++c, ++it) {
           const int sl = it % Cfg::kSlots;
@@ -394,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
       uint32_t ph = 0, sph = 0;
       bool ok = true;
       for (int i = pair; i < num_tiles && ok; i += pairs) {
-        const Tile t = tile_at<kMode>(p, i, 0);
+        const Tile t = tile_at<kMode>(p, buffer, i, 0);
         if (t.nkb == 0) continue;
         uint32_t d = tmem + static_cast<uint32_t>(Cfg::kAccStep * (done & 1));
         const int end = t.kb0 + t.nkb;
@@ -500,7 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
     int done = 0;
     bool ok = true;
     for (int i = pair; i < num_tiles && ok; i += pairs) {
-      const Tile t = tile_at<kMode>(p, i, rank);
+      const Tile t = tile_at<kMode>(p, buffer, i, rank);
       const int rows = t.rows - 32 * q;                    // of this warp's 32
       const int64_t y_row = t.y_row + 32 * q;
       if (t.nkb == 0) {                                    // an expert without tokens: a zero gradient
@@ -604,7 +674,7 @@ static int resident_pairs(const void* fn) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (sm_count() / 2)));
   cfg.blockDim = dim3(Cfg::kThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes + sizeof(Buffer);
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) n = sm_count() / 2;
   cache[{dev, fn}] = n;
@@ -640,13 +710,16 @@ static cudaError_t gemm_t(const Fp8GemmArgs& a, cudaStream_t s) {
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
   p.num_tiles = static_cast<int>(tiles);
   p.a_oob = static_cast<int>(blocks128(a.a_rows) * 128);
+  p.E = a.E;
+  p.counts = a.counts;
   if (a.table) p.t = *a.table;
   p.Y = a.Y;
   p.flags = a.flags;
   p.status = a.status;
   auto kern = fp8_gemm_kernel<kMode, kBf16Out>;
   const void* fn = reinterpret_cast<const void*>(kern);
-  cudaError_t e = set_max_dynamic_smem(fn, Cfg::kSmemBytes);
+  const size_t smem = Cfg::kSmemBytes + (kMode == Fp8GemmArgs::kRows ? sizeof(Buffer) : 0);
+  cudaError_t e = set_max_dynamic_smem(fn, smem);
   if (e != cudaSuccess) return e;
   // one pair per two SMs that can hold pairs at once
   int most = resident_pairs(fn);
@@ -666,7 +739,7 @@ static cudaError_t gemm_t(const Fp8GemmArgs& a, cudaStream_t s) {
     }
   }
   const int pairs = p.num_tiles < most ? p.num_tiles : most;
-  return launch_ex(kern, dim3(2 * pairs), dim3(Cfg::kThreads), Cfg::kSmemBytes, s, true, ma, mb, msa, msb, my, p);
+  return launch_ex(kern, dim3(2 * pairs), dim3(Cfg::kThreads), smem, s, true, ma, mb, msa, msb, my, p);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t s) {

@@ -22,7 +22,7 @@ constexpr int kTableThreads = 1024;
 
 __global__ void __launch_bounds__(kTableThreads) fp8_table_kernel(const int32_t* counts, int E, int64_t l_cap,
                                                                   const Fp8Table t, uint32_t* status) {
-  __shared__ int32_t s_rows[kMaxExperts], s_blk[kMaxExperts], s_tile[kMaxExperts];   // rows; ends in blocks, tiles
+  __shared__ int32_t s_rows[kMaxExperts], s_blk[kMaxExperts];   // rows; ends in blocks
   __shared__ uint64_t s_warp[32];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
@@ -30,12 +30,8 @@ __global__ void __launch_bounds__(kTableThreads) fp8_table_kernel(const int32_t*
   const int32_t n = tid < E ? __ldg(counts + tid) : 0;
   const bool bad = n < 0 || n > l_cap;
   const bool any_bad = __syncthreads_or(bad) != 0;
-  // blocks in the low 35 bits of a word (1024 counts of at most 2^24 blocks),
-  // tiles above them: when the segments fit there are at most 2^24 tiles
-  constexpr int kShift = 35;
-  constexpr uint64_t kLow = (1ull << kShift) - 1;
   const uint64_t blk = bad ? 0 : (static_cast<uint64_t>(n) + 127) / 128;
-  uint64_t x = blk | (((blk + 1) / 2) << kShift);
+  uint64_t x = blk;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint64_t y = __shfl_up_sync(kFull, x, o);
@@ -54,20 +50,16 @@ __global__ void __launch_bounds__(kTableThreads) fp8_table_kernel(const int32_t*
   }
   __syncthreads();
   if (warp > 0) x += s_warp[warp - 1];
-  const uint64_t all = s_warp[31];
   const int64_t n_blocks = l_cap / 128;
-  const bool fits = !any_bad && static_cast<int64_t>(all & kLow) <= n_blocks;
-  const int32_t blocks = fits ? static_cast<int32_t>(all & kLow) : 0;
-  const int32_t tiles = fits ? static_cast<int32_t>(all >> kShift) : 0;
+  const bool fits = !any_bad && static_cast<int64_t>(s_warp[31]) <= n_blocks;
+  const int32_t blocks = fits ? static_cast<int32_t>(s_warp[31]) : 0;
   if (tid < E) s_rows[tid] = n;
   if (tid < E && fits) {
-    s_blk[tid] = static_cast<int32_t>(x & kLow);
-    s_tile[tid] = static_cast<int32_t>(x >> kShift);
-    t.seg[tid] = Fp8Seg{static_cast<int32_t>(128 * ((x & kLow) - blk)), n};
+    s_blk[tid] = static_cast<int32_t>(x);
+    t.seg[tid] = Fp8Seg{static_cast<int32_t>(128 * (x - blk)), n};
   }
   if (tid == 0) {
-    t.totals[0] = tiles;
-    t.totals[1] = fits ? 1 : 0;
+    *t.fits = fits ? 1 : 0;
     if (!fits) raise_status(status, AVR_ERR_INVALID_ARG);
   }
   __syncthreads();
@@ -89,12 +81,6 @@ __global__ void __launch_bounds__(kTableThreads) fp8_table_kernel(const int32_t*
     return lo;
   };
   for (int32_t b = tid; b < n_blocks; b += kTableThreads) t.block_expert[b] = b < blocks ? find(s_blk, b) : -1;
-  for (int32_t i = tid; i < tiles; i += kTableThreads) {
-    const int e = find(s_tile, i);
-    const int32_t first_tile = e > 0 ? s_tile[e - 1] : 0, first_blk = e > 0 ? s_blk[e - 1] : 0;
-    const int32_t off = 256 * (i - first_tile);
-    t.tiles[i] = Fp8Tile{128 * first_blk + off, e, min(256, s_rows[e] - off), 0};
-  }
 }
 
 cudaError_t launch_fp8_table(const int32_t* counts, int E, int64_t l_cap, const Fp8Table& t, uint32_t* status,
@@ -120,7 +106,7 @@ __global__ void __launch_bounds__(kQThreads, 4) fp8_quant_kernel(const Fp8QuantA
   constexpr int N = In<kBf16>::kN, Q = 16 / N;
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
-  if (kMode == Rows::kGrouped && __ldcg(t.totals + 1) == 0) return;
+  if (kMode == Rows::kGrouped && __ldcg(t.fits) == 0) return;
   const int lane = threadIdx.x & 31;
   const uint4* X = static_cast<const uint4*>(a.X);
   const int64_t V = a.K / N;
@@ -214,7 +200,7 @@ __global__ void __launch_bounds__(kQThreads) fp8_quant_tokens_kernel(const Fp8Qu
   const int64_t f0 = blockIdx.x % ftiles * F, c = blockIdx.x / ftiles;   // feature tiles fastest: they share rows
   int64_t end = a.rows;
   if (a.table != nullptr) {
-    if (__ldcg(t.totals + 1) == 0) return;
+    if (__ldcg(t.fits) == 0) return;
     const int e = __ldcg(t.block_expert + c);
     if (e < 0) return;
     const int2 sg = __ldcg(reinterpret_cast<const int2*>(t.seg + e));

@@ -57,21 +57,16 @@ inline size_t fp8_scales_bytes(int64_t rows, int64_t K) {
   return static_cast<size_t>(blocks128(rows)) * static_cast<size_t>(atoms128(K)) * 512;
 }
 
-// The experts' buffer as the 8-bit kernels see it, from the counts: segments,
-// the expert of every 128-row block (-1 past the last), and the product's row
-// tiles: up to 256 rows of one expert.
+// The experts' buffer as the quantizers and the weight gradients see it, from
+// the counts: segments, and the expert of every 128-row block (-1 past the last).
 struct Fp8Seg {
   int32_t row0, rows;
-};
-struct Fp8Tile {
-  int32_t row0, expert, rows, pad;     // rows holding tokens, 1 .. 256
 };
 struct Fp8Table {
   Fp8Seg* seg;              // [E]
   int32_t* block_expert;    // [l_cap / 128]
-  Fp8Tile* tiles;           // [l_cap / 128]
   int32_t* order;           // [E] experts, the ones with the most tokens first
-  int32_t* totals;          // {tiles, 1 when the segments fit}
+  int32_t* fits;            // 1 when the segments fit, else 0
 };
 cudaError_t launch_fp8_table(const int32_t* counts, int E, int64_t l_cap, const Fp8Table& t, uint32_t* status,
                              cudaStream_t s);
@@ -113,10 +108,12 @@ struct Fp8GemmArgs {
   avr_dtype yt;
   uint32_t* flags;
   uint32_t* status;
-  // one product; the row tiles of the experts' buffer, B = the experts stacked;
-  // or one product per expert along its tokens, Y = the experts stacked
+  // one product; the row tiles of the experts' buffer, B = the experts stacked
+  // (counts); or one product per expert along its tokens, Y = the experts
+  // stacked (table)
   enum Mode { kDense, kRows, kTokens } mode = kDense;
   int E = 1;
+  const int32_t* counts = nullptr;
   const Fp8Table* table = nullptr;
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t s);
