@@ -49,13 +49,12 @@
 #include <map>
 #include <mutex>
 
-#include "device.cuh"
-#include "pair.cuh"
-#include "route.h"
+#include "fp8_pair.cuh"
 
 namespace avr {
 
 using namespace pair;
+using namespace fp8;
 
 namespace {
 
@@ -116,63 +115,6 @@ struct Tile {
   int32_t part;                   // kDense: which part of the tile (0: all, or the first)
 };
 
-// kRows: the experts' buffer in shared memory
-struct Buffer {
-  int32_t rows[kMaxExperts];       // tokens
-  int32_t blk_end[kMaxExperts];    // 128-row blocks up to and with this expert
-  int32_t tile_end[kMaxExperts];   // 256-row tiles likewise
-  uint64_t warp[32];
-};
-
-// Fills it from the counts, by the whole CTA; the number of row tiles, 0 when
-// the segments do not fit l_cap rows.
-__device__ __forceinline__ int scan_counts(const int32_t* counts, int E, int64_t l_cap, Buffer* b, uint32_t* status) {
-  static_assert(2 * Cfg::kThreads >= kMaxExperts, "two experts a thread");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int32_t n[2];
-  uint64_t x[2];
-  bool bad = false;
-  // blocks in the low 35 bits of a word (1024 counts of at most 2^24 blocks),
-  // tiles above them: when the segments fit there are at most 2^24 tiles
-  constexpr int kShift = 35;
-  constexpr uint64_t kLow = (1ull << kShift) - 1;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    n[i] = 2 * tid + i < E ? __ldcg(counts + 2 * tid + i) : 0;
-    const bool out = n[i] < 0 || n[i] > l_cap;
-    bad |= out;
-    const uint64_t blk = out ? 0 : (static_cast<uint64_t>(n[i]) + 127) / 128;
-    x[i] = blk | (((blk + 1) / 2) << kShift);
-  }
-  uint64_t sum = x[0] + x[1];
-  const uint64_t own = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-    if (lane >= o) sum += y;
-  }
-  if (lane == 31) b->warp[warp] = sum;
-  const bool any_bad = __syncthreads_or(bad) != 0;
-  uint64_t before = sum - own, all = 0;
-  for (int w = 0; w < Cfg::kThreads / 32; ++w) {
-    before += w < warp ? b->warp[w] : 0;
-    all += b->warp[w];
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    before += x[i];
-    if (2 * tid + i < E) {
-      b->rows[2 * tid + i] = n[i];
-      b->blk_end[2 * tid + i] = static_cast<int32_t>(before & kLow);
-      b->tile_end[2 * tid + i] = static_cast<int32_t>(before >> kShift);
-    }
-  }
-  const bool fits = !any_bad && static_cast<int64_t>(all & kLow) <= l_cap / 128;
-  if (!fits && blockIdx.x == 0 && tid == 0) raise_status(status, AVR_ERR_INVALID_ARG);
-  __syncthreads();
-  return fits ? static_cast<int>(all >> kShift) : 0;
-}
-
 template <int kMode>
 __device__ __forceinline__ Tile tile_at(const Params& p, const Buffer* b, int i, int rank) {
   Tile t;
@@ -198,15 +140,7 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const Buffer* b, int i,
     t.y_row = m0;
     t.rows = static_cast<int32_t>(min64(128, p.M - m0));
   } else if (kMode == Fp8GemmArgs::kRows) {
-    const int mt = i / p.tiles_n;
-    int lo = 0, hi = p.E - 1;                            // the first expert whose tiles end past mt
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (b->tile_end[mid] > mt)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
+    const int mt = i / p.tiles_n, lo = expert_of_tile(b, p.E, mt);
     const int off = 256 * (mt - (lo > 0 ? b->tile_end[lo - 1] : 0));
     const int row0 = 128 * (lo > 0 ? b->blk_end[lo - 1] : 0) + off + rank * 128;
     t.n0 = i % p.tiles_n * 256;
@@ -244,27 +178,6 @@ __device__ __forceinline__ int visit_length(int n) {
   return kBf16Out || visits < 2 ? n : (n + visits - 1) / visits;
 }
 
-// TMA 2-D load into this CTA's shared memory, completing on the barrier at a
-// shared::cluster address in either CTA of the pair
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int32_t x,
-                                                 int32_t y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
-      : "memory");
-}
-
-// One lane of a converged warp.  The compiler knows that the branch on it has
-// one thread, which a branch on the lane number does not tell it: issued from
-// the latter, the MMAs, commits and copies of a stage took about 290 ns more
-// (8192 x 1024 x 4096: 36.8 -> 27.6 us).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
 // TMA reduction shared -> global: adds, each element rounded to nearest
 __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
   asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%2, %3}], [%1];"
@@ -292,17 +205,6 @@ __device__ __forceinline__ bool flag_take(uint32_t* f, uint32_t* status) {
   *f = 0u;
   fence_proxy_async_global();
   return true;
-}
-
-__device__ __forceinline__ void mma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t"
-      "}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
-      : "memory");
 }
 
 }  // namespace
@@ -372,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
   const int pairs = static_cast<int>(gridDim.x) / 2, pair = static_cast<int>(blockIdx.x) / 2;
   int num_tiles = p.num_tiles;
   Buffer* buffer = reinterpret_cast<Buffer*>(smem_raw + Cfg::kSmemBytes);
-  if (kMode == Fp8GemmArgs::kRows) num_tiles = scan_counts(p.counts, p.E, p.M, buffer, p.status) * p.tiles_n;
+  if (kMode == Fp8GemmArgs::kRows) num_tiles = scan_counts<Cfg::kThreads, 2>(p.counts, p.E, p.M, buffer, p.status) * p.tiles_n;
   if (kMode == Fp8GemmArgs::kTokens && __ldcg(p.t.fits) == 0) num_tiles = 0;   // the counts did not fit
   // both CTAs of a pair leave their loops together: a CTA whose shared memory
   // is misaligned has a misaligned partner (same launch), so neither works
@@ -663,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
 
 // Clusters of two CTAs of `fn` that can be resident at once on the current
 // device (cached per device and function).
-static int resident_pairs(const void* fn) {
+int fp8_resident_pairs(const void* fn, int threads, size_t smem) {
   static std::mutex mu;
   static std::map<std::pair<int, const void*>, int> cache;
   int dev = 0;
@@ -673,8 +575,8 @@ static int resident_pairs(const void* fn) {
   if (it != cache.end()) return it->second;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (sm_count() / 2)));
-  cfg.blockDim = dim3(Cfg::kThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmemBytes + sizeof(Buffer);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) n = sm_count() / 2;
   cache[{dev, fn}] = n;
@@ -722,7 +624,7 @@ static cudaError_t gemm_t(const Fp8GemmArgs& a, cudaStream_t s) {
   cudaError_t e = set_max_dynamic_smem(fn, smem);
   if (e != cudaSuccess) return e;
   // one pair per two SMs that can hold pairs at once
-  int most = resident_pairs(fn);
+  int most = fp8_resident_pairs(fn, Cfg::kThreads, smem);
   if (most > kFp8MaxPairs) most = kFp8MaxPairs;
   p.cut0 = 0x7FFFFFFF;
   p.parts = 1;
@@ -743,6 +645,7 @@ static cudaError_t gemm_t(const Fp8GemmArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t s) {
+  if (fp8_stream_applies(a)) return launch_fp8_stream(a, s);
   const bool b = a.yt == AVR_BF16;
   switch (a.mode) {
     case Fp8GemmArgs::kDense: return b ? gemm_t<Fp8GemmArgs::kDense, true>(a, s) : gemm_t<Fp8GemmArgs::kDense, false>(a, s);

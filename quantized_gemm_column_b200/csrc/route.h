@@ -117,6 +117,13 @@ struct Fp8GemmArgs {
   const Fp8Table* table = nullptr;
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t s);
+constexpr int kFp8MaxVisit = 48;     // blocks of K that one fp32 accumulation spans
+// the experts' products with few rows an expert (fp8_stream.cu): kRows
+constexpr int64_t kStreamBlocks = 2;
+bool fp8_stream_applies(const Fp8GemmArgs& a);
+cudaError_t launch_fp8_stream(const Fp8GemmArgs& a, cudaStream_t s);
+// clusters of two CTAs of `fn` that can be resident at once on the current device (cached)
+int fp8_resident_pairs(const void* fn, int threads, size_t smem);
 
 // ---------------- 8-bit linear layer of a few tokens (fp8_skinny.cu) ----------------
 // Y [l, N] = Q(X) w^T, w [N, K]

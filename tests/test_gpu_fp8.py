@@ -369,6 +369,35 @@ def test_experts_forward_and_gradients(api, counts, m, n, dt, ot):
     assert (Y[torch.from_numpy(free)] == 7.0).all() and (dX[torch.from_numpy(free)] == 7.0).all()
 
 
+@pytest.mark.parametrize("counts", [[3, 0, 1, 32, 33, 64, 0, 0], [1] + [0] * 7, [0, 0, 300, 0, 0, 0, 1, 0, 0, 97, 128, 0],
+                                    [2] * 40, [0] * 5, [128] * 4, [100, 120, 1, 0, 65, 31, 0, 129, 0, 7]])
+@pytest.mark.parametrize("m,n,dt,ot", [(128, 128, "bf16", "bf16"), (640, 384, "f32", "f32"), (1408, 256, "bf16", "bf16"),
+                                       (6272, 128, "bf16", "f32")])
+def test_experts_few_rows(api, counts, m, n, dt, ot):
+    """A few rows an expert, as in decoding: the weights are on the instruction's
+    row side; rows without a token are neither read nor written."""
+    E = len(counts)
+    X, off = _buffer(counts, m, dt, 3, extra=128 if sum(-(-c // 128) for c in counts) < E else 0)
+    cap = X.shape[0]
+    assert cap <= 128 * E
+    ws = api.fp8_moe_workspace(cap, m, n, E)
+    w, f, d = _experts(api, E, m, n, dt, ws)
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    Y = torch.full((cap, n), 7.0, dtype=DT[ot], device="cuda")
+    api.fp8_moe_linear_fwd(X.cuda(), cnt, f, Y, ws)
+    D, _ = _buffer(counts, n, dt, 4, extra=cap - _segments(counts)[1])
+    dX = torch.full((cap, m), 7.0, dtype=DT[ot], device="cuda")
+    api.fp8_moe_linear_dgrad(D.cuda(), cnt, d, dX, ws)
+    assert api.averis_check_status(ws) == 0
+    free = torch.ones(cap, dtype=torch.bool)
+    for e, (o, c) in enumerate(zip(off, counts)):
+        free[o:o + c] = False
+        if c:
+            _check_product(Y[o:o + c], R.deq(X[o:o + c].double().numpy()), w[e].T, m)
+            _check_product(dX[o:o + c], R.deq(D[o:o + c].double().numpy()), w[e], n)
+    assert (Y.cpu()[free] == 7.0).all() and (dX.cpu()[free] == 7.0).all()
+
+
 def test_experts_weights_bit_exact(api):
     E, m, n = 3, 256, 384
     ws = api.fp8_moe_workspace(0, m, n, E)
