@@ -495,8 +495,8 @@ avr_status fp8_quant_t(const void* X, avr_dtype xt, int64_t l, int64_t K, const 
                        size_t ws_bytes, avr_stream stream);
 
 /* W [m, n] in 128 x 128 blocks for both products: w_fwd = Q(W)^T [n, m] and
- * w_dgrad = Q(W) [m, n] (nullable), the same codes and scales.  Launches 1
- * kernel. */
+ * w_dgrad = Q(W) [m, n] (nullable), the same codes and scales.  m <= 65535 *
+ * 128.  Launches 1 kernel. */
 avr_status fp8_quant_weight(const void* W, avr_dtype wt, int64_t m, int64_t n, const avr_fp8* w_fwd,
                             const avr_fp8* w_dgrad, void* ws, size_t ws_bytes, avr_stream stream);
 
@@ -506,8 +506,9 @@ avr_status fp8_gemm(const avr_fp8* a, const avr_fp8* b, void* Y, avr_dtype yt, v
                     avr_stream stream);
 
 /* Y [l, n] = Q(X) Q(W), dX [l, m] = Q(D) Q(W)^T, dW [m, n] = Q(X^T) Q(D^T)^T
- * (0 when l = 0).  Launch 2, 2 and 3 kernels; the first two 1 for a few
- * tokens, whose sums then have another order. */
+ * (0 when l = 0).  Launch 2 kernels each (the last 3 when X and D are
+ * large or have different types); the first two 1 for a few tokens, whose
+ * sums then have another order. */
 avr_status fp8_linear_fwd(const void* X, avr_dtype xt, int64_t l, int64_t m, int64_t n, const avr_fp8* w_fwd, void* Y,
                           avr_dtype yt, void* ws, size_t ws_bytes, avr_stream stream);
 avr_status fp8_linear_dgrad(const void* D, avr_dtype dt, int64_t l, int64_t m, int64_t n, const avr_fp8* w_dgrad,
@@ -539,7 +540,8 @@ avr_status fp8_moe_gemm(const avr_fp8* xq, const int32_t* counts, int E, const a
 
 /* Per expert: Y = Q(X) Q(W_e), dX = Q(D) Q(W_e)^T, dW [E][m][n] = Q(X^T)
  * Q(D^T)^T over the expert's tokens (0 where it has none).  X [l_cap, m],
- * D [l_cap, n].  Launch 3, 3 and 4 kernels. */
+ * D [l_cap, n].  Launch 3 kernels each (the last 4 when X and D are
+ * large or have different types). */
 avr_status fp8_moe_linear_fwd(const void* X, avr_dtype xt, int64_t l_cap, const int32_t* counts, int E, int64_t m,
                               int64_t n, const avr_fp8* w_fwd, void* Y, avr_dtype yt, void* ws, size_t ws_bytes,
                               avr_stream stream);

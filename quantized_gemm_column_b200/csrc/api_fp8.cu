@@ -311,11 +311,12 @@ avr_status fp8_quant_t(const void* X, avr_dtype xt, int64_t l, int64_t K, const 
   if (!aligned16(X)) return AVR_ERR_MISALIGNED;
   AVR_TRY(check_ws(ws, ws_bytes, kScratch));
   AVR_TRY(device_ok());
-  return cuda_status(launch_fp8_quant_t(quant_args(X, xt, l, K, out->codes, out->scales, ws), stream));
+  return cuda_status(launch_fp8_quant_t(quant_args(X, xt, l, K, out->codes, out->scales, ws), nullptr, stream));
 }
 
 static avr_status quant_weights(const void* W, avr_dtype wt, int E, int64_t m, int64_t n, const avr_fp8* w_fwd,
                                 const avr_fp8* w_dgrad, void* ws, size_t ws_bytes, avr_stream stream) {
+  if (blocks128(m) > kFp8MaxWeightBlocks) return AVR_ERR_UNSUPPORTED_SHAPE;
   if (!W) return AVR_ERR_INVALID_ARG;
   AVR_TRY(check_fp8(w_fwd, E * n, m));
   if (w_dgrad) AVR_TRY(check_fp8(w_dgrad, E * m, n));
@@ -373,8 +374,8 @@ avr_status fp8_linear_wgrad(const void* X, avr_dtype xt, const void* D, avr_dtyp
                                                   (wt == AVR_BF16 ? 2 : 4), stream));
   uint8_t *xc = at<uint8_t>(ws, lay.xt_codes), *xs = at<uint8_t>(ws, lay.xt_scales);
   uint8_t *dc = at<uint8_t>(ws, lay.dt_codes), *ds = at<uint8_t>(ws, lay.dt_scales);
-  AVR_TRY(cuda_status(launch_fp8_quant_t(quant_args(X, xt, l, m, xc, xs, ws), stream)));
-  AVR_TRY(cuda_status(launch_fp8_quant_t(quant_args(D, dt, l, n, dc, ds, ws), stream)));
+  const Fp8QuantArgs qx = quant_args(X, xt, l, m, xc, xs, ws), qd = quant_args(D, dt, l, n, dc, ds, ws);
+  AVR_TRY(cuda_status(launch_fp8_quant_t(qx, &qd, stream)));
   return cuda_status(
       launch_fp8_gemm(gemm_args(xc, xs, m, dc, ds, n, blocks128(l) * 128, m, n, dW, m, wt, ws), stream));
 }
@@ -456,12 +457,10 @@ avr_status fp8_moe_linear_wgrad(const void* X, avr_dtype xt, const void* D, avr_
                                                   static_cast<size_t>(n) * (wt == AVR_BF16 ? 2 : 4), stream));
   uint8_t *xc = at<uint8_t>(ws, lay.xt_codes), *xs = at<uint8_t>(ws, lay.xt_scales);
   uint8_t *dc = at<uint8_t>(ws, lay.dt_codes), *ds = at<uint8_t>(ws, lay.dt_scales);
-  Fp8QuantArgs q = quant_args(X, xt, l_cap, m, xc, xs, ws);
-  q.table = &table;
-  AVR_TRY(cuda_status(launch_fp8_quant_t(q, stream)));
-  q = quant_args(D, dt, l_cap, n, dc, ds, ws);
-  q.table = &table;
-  AVR_TRY(cuda_status(launch_fp8_quant_t(q, stream)));
+  Fp8QuantArgs qx = quant_args(X, xt, l_cap, m, xc, xs, ws), qd = quant_args(D, dt, l_cap, n, dc, ds, ws);
+  qx.table = &table;
+  qd.table = &table;
+  AVR_TRY(cuda_status(launch_fp8_quant_t(qx, &qd, stream)));
   Fp8GemmArgs g = gemm_args(xc, xs, m, dc, ds, n, l_cap, m, n, dW, static_cast<int64_t>(E) * m, wt, ws);
   g.mode = Fp8GemmArgs::kTokens;
   g.E = E;

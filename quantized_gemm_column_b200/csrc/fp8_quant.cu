@@ -10,6 +10,7 @@
 // the non-finite check fall out of them.
 #include "fp8_common.cuh"
 #include "route.h"
+#include "strips.cuh"
 
 namespace avr {
 
@@ -93,7 +94,7 @@ cudaError_t launch_fp8_table(const int32_t* counts, int E, int64_t l_cap, const 
 // eight lanes share a block and the warp's four scale bytes are one word of an
 // atom.  kRows rows' loads are in flight at once, four of bf16 or two of fp32
 // (64 bytes a lane and row), with four blocks an SM: 16384 x 6144 bf16 takes
-// 47 us (6.4 TB/s), with two rows 50; 4133 x 2000 fp32 8.4 us, with four 17
+// 46 us (6.6 TB/s), with two rows 50; 4133 x 2000 fp32 8.4 us, with four 17
 // ---------------------------------------------------------------------------
 constexpr int kQThreads = 256;
 constexpr int kQWarps = kQThreads / 32;
@@ -113,9 +114,10 @@ __global__ void __launch_bounds__(kQThreads, 4) fp8_quant_kernel(const Fp8QuantA
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kQWarps;
   const int64_t tasks = (rows_pad / kRows) * strips;
   bool bad = false;
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kQWarps + (threadIdx.x >> 5); task < tasks; task += warps) {
-    const int strip = static_cast<int>(task % strips);
-    const int64_t r0 = task / strips * kRows;
+  for (StripWalk at(static_cast<int64_t>(blockIdx.x) * kQWarps + (threadIdx.x >> 5), warps, tasks, strips); at.more();
+       at.step()) {
+    const int strip = at.strip;
+    const int64_t r0 = at.row * kRows;
     const int64_t col = static_cast<int64_t>(strip) * 512 + 16 * lane;
     int64_t end = a.rows;
     if (kMode == Rows::kGrouped) {        // a task lies in one 128-row block, so in one segment
@@ -185,19 +187,17 @@ cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, cudaStream_t s) {
 // 32 fp32).  A thread holds four consecutive tokens of one vector, so its
 // codes of a feature are one word of the transposed tile; the tile goes
 // through shared memory (rows of 33 words) and out as full 128-byte lines.
-// 16384 x 6144 bf16: 52 us (5.8 TB/s).
+// 16384 x 6144 bf16: 54 us (5.6 TB/s).
 // ---------------------------------------------------------------------------
 template <bool kBf16>
-__global__ void __launch_bounds__(kQThreads) fp8_quant_tokens_kernel(const Fp8QuantArgs a, const Fp8Table t,
-                                                                     int64_t L, int64_t atoms, unsigned ftiles) {
+__device__ __forceinline__ void quant_tokens(const Fp8QuantArgs& a, const Fp8Table& t, int64_t L, int64_t atoms,
+                                             unsigned ftile, int64_t c) {
   constexpr int N = In<kBf16>::kN, F = 8 * N;
   __shared__ uint32_t s_max[kQWarps][32];            // maxima, a word as in the input
   __shared__ uint32_t s_byte[F];
   __shared__ uint32_t s_tile[F][33];
-  pdl_wait_prior_grid();
-  pdl_allow_next_grid();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t f0 = blockIdx.x % ftiles * F, c = blockIdx.x / ftiles;   // feature tiles fastest: they share rows
+  const int64_t f0 = static_cast<int64_t>(ftile) * F;
   int64_t end = a.rows;
   if (a.table != nullptr) {
     if (__ldcg(t.fits) == 0) return;
@@ -253,22 +253,63 @@ __global__ void __launch_bounds__(kQThreads) fp8_quant_tokens_kernel(const Fp8Qu
     if (f0 + f < a.K) *reinterpret_cast<uint32_t*>(a.codes + (f0 + f) * L + c * 128 + 4 * lane) = s_tile[f][lane];
 }
 
-cudaError_t launch_fp8_quant_t(const Fp8QuantArgs& a, cudaStream_t s) {
-  const int64_t L = blocks128(a.rows) * 128;
+// Feature tiles are the grid's x: they share the tokens' rows.  The blocks are
+// short, so a division of the block index would show (54 us become 58).
+template <bool kBf16>
+__global__ void __launch_bounds__(kQThreads) fp8_quant_tokens_kernel(const Fp8QuantArgs a, const Fp8Table t,
+                                                                     int64_t L, int64_t atoms) {
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int64_t c = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
+  if (c * 128 < L) quant_tokens<kBf16>(a, t, L, atoms, blockIdx.x, c);
+}
+
+// two tensors over the same tokens: ftiles0 feature tiles of the first, then the second's
+template <bool kBf16>
+__global__ void __launch_bounds__(kQThreads)
+    fp8_quant_tokens2_kernel(const Fp8QuantArgs a0, const Fp8QuantArgs a1, const Fp8Table t, int64_t L, int64_t atoms,
+                             unsigned ftiles0) {
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int64_t c = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
+  if (c * 128 >= L) return;
+  if (blockIdx.x < ftiles0)
+    quant_tokens<kBf16>(a0, t, L, atoms, blockIdx.x, c);
+  else
+    quant_tokens<kBf16>(a1, t, L, atoms, blockIdx.x - ftiles0, c);
+}
+
+// Two tensors in one launch save the second's start and end, about 2 us, which
+// counts while they are small: 3300 blocks of 4133 tokens fp32 13 us, in two
+// launches 16; larger ones go one after the other.
+constexpr int64_t kTwoBlocks = 8192;
+
+cudaError_t launch_fp8_quant_t(const Fp8QuantArgs& a, const Fp8QuantArgs* b, cudaStream_t s) {
   const int F = a.xt == AVR_BF16 ? 64 : 32;
-  const int64_t ftiles = blocks128(a.K) * 128 / F, grid = ftiles * (L / 128);
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const int64_t L = blocks128(a.rows) * 128;
+  const int64_t ftiles0 = blocks128(a.K) * 128 / F, ftiles = ftiles0 + (b ? blocks128(b->K) * 128 / F : 0);
+  const int64_t grid = ftiles * (L / 128);
+  if (b != nullptr && (b->xt != a.xt || grid > kTwoBlocks)) {
+    cudaError_t e = launch_fp8_quant_t(a, nullptr, s);
+    return e != cudaSuccess ? e : launch_fp8_quant_t(*b, nullptr, s);
+  }
   const Fp8Table t = a.table ? *a.table : Fp8Table{};
-  auto kern = a.xt == AVR_BF16 ? fp8_quant_tokens_kernel<true> : fp8_quant_tokens_kernel<false>;
-  return launch_ex(kern, dim3(static_cast<unsigned>(grid)), dim3(kQThreads), 0, s, true, a, t, L, atoms128(L),
-                   static_cast<unsigned>(ftiles));
+  const int64_t blocks = L / 128, z = (blocks + 65534) / 65535;        // at most 2^24 blocks
+  const dim3 g(static_cast<unsigned>(ftiles), static_cast<unsigned>((blocks + z - 1) / z), static_cast<unsigned>(z));
+  const dim3 threads(kQThreads);
+  if (b == nullptr) {
+    auto kern = a.xt == AVR_BF16 ? fp8_quant_tokens_kernel<true> : fp8_quant_tokens_kernel<false>;
+    return launch_ex(kern, g, threads, 0, s, true, a, t, L, atoms128(L));
+  }
+  auto kern = a.xt == AVR_BF16 ? fp8_quant_tokens2_kernel<true> : fp8_quant_tokens2_kernel<false>;
+  return launch_ex(kern, g, threads, 0, s, true, a, *b, t, L, atoms128(L), static_cast<unsigned>(ftiles0));
 }
 
 // ---------------------------------------------------------------------------
 // weights: a CTA takes one 128 x 128 block and writes it both ways round, the
 // transposed codes through shared memory.  A block loads, then computes, then
 // stores, so it takes four on an SM to keep memory busy: 64 x 2048 x 1024 bf16
-// in 91 us (5.9 TB/s), 114 with the registers for three
+// in 84 us (6.4 TB/s); 114 with the registers for three
 // ---------------------------------------------------------------------------
 template <bool kBf16>
 __global__ void __launch_bounds__(kQThreads, kBf16 ? 4 : 2)
@@ -282,8 +323,8 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 4 : 2)
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t bns = (n + 127) / 128, bms = (m + 127) / 128;
-  const int64_t bn = blockIdx.x % bns, bm = blockIdx.x / bns % bms, e = blockIdx.x / bns / bms;
+  const int64_t bns = gridDim.x, bms = gridDim.y;
+  const int64_t bn = blockIdx.x, bm = blockIdx.y, e = blockIdx.z;
   const int v = tid % kCols, g = tid / kCols;
   const uint4* X = static_cast<const uint4*>(W) + e * m * (n / N);
   const int64_t V = n / N, vec = bn * kCols + v;
@@ -359,10 +400,10 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 4 : 2)
 cudaError_t launch_fp8_quant_weight(const void* W, avr_dtype wt, int E, int64_t m, int64_t n, uint8_t* fwd_codes,
                                     uint8_t* fwd_scales, uint8_t* dg_codes, uint8_t* dg_scales, uint32_t* status,
                                     cudaStream_t s) {
-  const int64_t grid = blocks128(n) * blocks128(m) * E;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  if (blocks128(m) > kFp8MaxWeightBlocks) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks128(n)), static_cast<unsigned>(blocks128(m)), static_cast<unsigned>(E));
   auto kern = wt == AVR_BF16 ? fp8_quant_weight_kernel<true> : fp8_quant_weight_kernel<false>;
-  return launch_ex(kern, dim3(static_cast<unsigned>(grid)), dim3(kQThreads), 0, s, true, W, m, n, fwd_codes, fwd_scales,
+  return launch_ex(kern, grid, dim3(kQThreads), 0, s, true, W, m, n, fwd_codes, fwd_scales,
                    dg_codes, dg_scales, atoms128(m), atoms128(n), status);
 }
 

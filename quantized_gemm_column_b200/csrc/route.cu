@@ -9,6 +9,7 @@
 
 #include "device.cuh"
 #include "route.h"
+#include "strips.cuh"
 
 namespace avr {
 
@@ -501,10 +502,11 @@ __global__ void __launch_bounds__(kPermThreads) dispatch_kernel(const PermuteArg
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kPermThreads / 32);
   const uint4* src = static_cast<const uint4*>(a.src);
   uint4* dst = static_cast<uint4*>(a.dst);
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * (kPermThreads / 32) + (threadIdx.x >> 5);
-       task < a.T * strips; task += warps) {
-    const int64_t t = task / strips;
-    const int64_t v0 = (task % strips) * (32 * kDispU) + lane;
+  for (StripWalk at(static_cast<int64_t>(blockIdx.x) * (kPermThreads / 32) + (threadIdx.x >> 5), warps, a.T * strips,
+                    strips);
+       at.more(); at.step()) {
+    const int64_t t = at.row;
+    const int64_t v0 = static_cast<int64_t>(at.strip) * (32 * kDispU) + lane;
     uint4 q[kDispU];
 #pragma unroll
     for (int u = 0; u < kDispU; ++u)
@@ -535,10 +537,11 @@ __global__ void __launch_bounds__(kPermThreads, 4) combine_kernel(const PermuteA
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kPermThreads / 32);
   const uint4* src = static_cast<const uint4*>(a.src);
   uint4* dst = static_cast<uint4*>(a.dst);
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * (kPermThreads / 32) + (threadIdx.x >> 5);
-       task < a.T * strips; task += warps) {
-    const int64_t t = task / strips;
-    const int64_t v0 = (task % strips) * (32 * kCombU) + lane;
+  for (StripWalk at(static_cast<int64_t>(blockIdx.x) * (kPermThreads / 32) + (threadIdx.x >> 5), warps, a.T * strips,
+                    strips);
+       at.more(); at.step()) {
+    const int64_t t = at.row;
+    const int64_t v0 = static_cast<int64_t>(at.strip) * (32 * kCombU) + lane;
     const int row = lane < a.k ? static_cast<int>(slot_row(a, t, lane)) : -1;
     const float weight = kWeighted && row >= 0 ? __ldg(a.weights + t * a.k + lane) : 0.0f;
     float acc[kCombU][N] = {};

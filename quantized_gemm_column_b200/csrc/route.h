@@ -84,9 +84,10 @@ struct Fp8QuantArgs {
   int64_t l_cap = 0;
 };
 cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, cudaStream_t s);
-// along the tokens: X [rows, K] -> [K, L], L = rows rounded up to 128
-cudaError_t launch_fp8_quant_t(const Fp8QuantArgs& a, cudaStream_t s);
-// W [E][m][n] -> fwd [E n, m], dgrad [E m, n] (nullable codes)
+// along the tokens: X [rows, K] -> [K, L], L = rows rounded up to 128; b: a second tensor over the same tokens
+cudaError_t launch_fp8_quant_t(const Fp8QuantArgs& a, const Fp8QuantArgs* b, cudaStream_t s);
+// W [E][m][n] -> fwd [E n, m], dgrad [E m, n] (nullable codes); m in 65535 blocks at most
+constexpr int64_t kFp8MaxWeightBlocks = 65535;
 cudaError_t launch_fp8_quant_weight(const void* W, avr_dtype wt, int E, int64_t m, int64_t n, uint8_t* fwd_codes,
                                     uint8_t* fwd_scales, uint8_t* dg_codes, uint8_t* dg_scales, uint32_t* status,
                                     cudaStream_t s);

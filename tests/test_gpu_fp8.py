@@ -235,6 +235,16 @@ def test_linear_forward_and_gradients(api, l, m, n, dt, ot):
     _check_product(dW, R.deq(x.T.copy()), R.deq(dd.T.copy()), l)
 
 
+@pytest.mark.parametrize("xt,dt", [("f32", "bf16"), ("bf16", "f32")])
+def test_weight_gradients_of_mixed_types(api, xt, dt):
+    l, m, n = 300, 144, 272
+    ws = api.fp8_workspace(l, m, n)
+    X, D, dW = _x(l, m, xt, 1, spread=False), _x(l, n, dt, 2, spread=False), torch.empty(m, n, device="cuda")
+    api.fp8_linear_wgrad(X.cuda(), D.cuda(), dW, ws)
+    assert api.averis_check_status(ws) == 0
+    _check_product(dW, R.deq(X.double().numpy().T.copy()), R.deq(D.double().numpy().T.copy()), l)
+
+
 @pytest.mark.parametrize("l", [1, 2, 4, 8, 16])
 def test_linear_extreme_scales(api, l):
     """Blocks whose scales' product leaves fp32's exponent range in parts only,
