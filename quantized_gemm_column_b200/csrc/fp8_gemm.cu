@@ -46,9 +46,6 @@
 // (kRows: a tile's rows belong to one expert, whose B is stacked); the
 // experts' weight gradients (kTokens: one product per expert, K = its tokens,
 // whose blocks may start at any byte of an atom).
-#include <map>
-#include <mutex>
-
 #include "fp8_pair.cuh"
 
 namespace avr {
@@ -563,23 +560,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::kThreads, 1)
   }
 }
 
-// Clusters of two CTAs of `fn` that can be resident at once on the current
-// device (cached per device and function).
-int fp8_resident_pairs(const void* fn, int threads, size_t smem) {
-  static std::mutex mu;
-  static std::map<std::pair<int, const void*>, int> cache;
+int fp8_resident_pairs(const void* fn, int threads, size_t smem, std::atomic<int>* cache) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  std::lock_guard<std::mutex> g(mu);
-  auto it = cache.find({dev, fn});
-  if (it != cache.end()) return it->second;
+  const bool kept = dev >= 0 && dev < kFp8CachedDevices;
+  int n = kept ? cache[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (sm_count() / 2)));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
-  int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) n = sm_count() / 2;
-  cache[{dev, fn}] = n;
+  if (kept) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -624,7 +616,8 @@ static cudaError_t gemm_t(const Fp8GemmArgs& a, cudaStream_t s) {
   cudaError_t e = set_max_dynamic_smem(fn, smem);
   if (e != cudaSuccess) return e;
   // one pair per two SMs that can hold pairs at once
-  int most = fp8_resident_pairs(fn, Cfg::kThreads, smem);
+  static std::atomic<int> resident[kFp8CachedDevices];
+  int most = fp8_resident_pairs(fn, Cfg::kThreads, smem, resident);
   if (most > kFp8MaxPairs) most = kFp8MaxPairs;
   p.cut0 = 0x7FFFFFFF;
   p.parts = 1;

@@ -15,9 +15,6 @@
 //
 // Roles as in fp8_gemm.cu: eight epilogue warps, an MMA thread and a scale
 // copier in the leading CTA, TMA producers of weights (two), of tokens and of scales.
-#include <map>
-#include <mutex>
-
 #include "fp8_pair.cuh"
 
 namespace avr {
@@ -361,7 +358,8 @@ static cudaError_t stream_t(const Fp8GemmArgs& a, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kern);
   cudaError_t e = set_max_dynamic_smem(fn, Cfg::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int most = fp8_resident_pairs(fn, Cfg::kThreads, Cfg::kSmemBytes);
+  static std::atomic<int> resident[kFp8CachedDevices];
+  const int most = fp8_resident_pairs(fn, Cfg::kThreads, Cfg::kSmemBytes, resident);
   const int pairs = static_cast<int>(tiles < most ? tiles : most);
   return launch_ex(kern, dim3(2 * pairs), dim3(Cfg::kThreads), Cfg::kSmemBytes, s, true, mw, mx, msw, msx, p);
 }

@@ -2,6 +2,8 @@
 // (fp8_quant.cu, fp8_gemm.cu) for their C entry points (api_fp8.cu).
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace avr {
@@ -123,8 +125,10 @@ constexpr int kFp8MaxVisit = 48;     // blocks of K that one fp32 accumulation s
 constexpr int64_t kStreamBlocks = 2;
 bool fp8_stream_applies(const Fp8GemmArgs& a);
 cudaError_t launch_fp8_stream(const Fp8GemmArgs& a, cudaStream_t s);
-// clusters of two CTAs of `fn` that can be resident at once on the current device (cached)
-int fp8_resident_pairs(const void* fn, int threads, size_t smem);
+// clusters of two CTAs of `fn` that can be resident at once on the current
+// device, kept per device in `cache` (zeros at first)
+constexpr int kFp8CachedDevices = 64;
+int fp8_resident_pairs(const void* fn, int threads, size_t smem, std::atomic<int>* cache);
 
 // ---------------- 8-bit linear layer of a few tokens (fp8_skinny.cu) ----------------
 // Y [l, N] = Q(X) w^T, w [N, K]

@@ -408,6 +408,35 @@ def test_experts_few_rows(api, counts, m, n, dt, ot):
     assert (Y.cpu()[free] == 7.0).all() and (dX.cpu()[free] == 7.0).all()
 
 
+@pytest.mark.parametrize("E,rows", [(257, 3), (1024, 2), (1000, 400)])
+def test_experts_many(api, E, rows):
+    """Up to 1024 experts: every one has few rows, or all rows are a few's."""
+    m = n = 128
+    rng = np.random.default_rng(E)
+    counts = rng.integers(0, rows + 1, E) if rows < 10 else np.zeros(E, dtype=np.int64)
+    counts[rng.integers(0, E, 4)] = 130 if rows < 10 else rows
+    counts = counts.tolist()
+    X, off = _buffer(counts, m, "bf16", 7)
+    D, _ = _buffer(counts, n, "bf16", 8)
+    cap = X.shape[0]
+    ws = api.fp8_moe_workspace(cap, m, n, E)
+    W = torch.randn(E, m, n, generator=torch.Generator().manual_seed(E)).bfloat16()
+    f = api.FP8Tensor(E * n, m)
+    api.fp8_moe_quant_weights(W.cuda(), f, None, ws)
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    Y, dW = torch.full((cap, n), 7.0, device="cuda"), torch.full((E, m, n), 7.0, device="cuda")
+    api.fp8_moe_linear_fwd(X.cuda(), cnt, f, Y, ws)
+    api.fp8_moe_linear_wgrad(X.cuda(), D.cuda(), cnt, dW, ws)
+    assert api.averis_check_status(ws) == 0
+    empty = torch.tensor([c == 0 for c in counts])
+    assert not dW.cpu()[empty].any()
+    for e in [e for e in range(E) if counts[e]][:: max(1, E // 40)]:
+        o, c = off[e], counts[e]
+        x, d = X[o:o + c].double().numpy(), D[o:o + c].double().numpy()
+        _check_product(Y[o:o + c], R.deq(x), R.deq(W[e].double().numpy(), (128, 128)).T, m)
+        _check_product(dW[e], R.deq(x.T.copy()), R.deq(d.T.copy()), c)
+
+
 def test_experts_weights_bit_exact(api):
     E, m, n = 3, 256, 384
     ws = api.fp8_moe_workspace(0, m, n, E)
@@ -471,3 +500,38 @@ def test_dispatch_quantizes_the_tokens_rows(api, T, k, E, K, dt):
     api.fp8_moe_dispatch(X.cuda(), bad, xq, ws)
     assert api.averis_check_status(ws) == api.AVR_ERR_INVALID_ARG
     _equal(xq, wq, wsb, rows=np.arange(cap))
+
+
+def test_offsets_past_32_bits(api):
+    """More than 2^31 elements in X, its codes, Y and the experts' buffer."""
+    l, m, n = 266000, 8192, 32
+    ws = api.fp8_workspace(l, m, n)
+    X = torch.zeros(l, m, dtype=torch.bfloat16, device="cuda")
+    f, W = api.FP8Tensor(n, m), _x(m, n, "f32", 1, spread=False)
+    api.fp8_quant_weight(W.cuda(), f, None, ws)
+    picks = [0, 1, 131072, 262143, 262144, 262145, l - 1]
+    X[picks] = _x(len(picks), m, "bf16", 2, spread=False).cuda()
+    Y = torch.full((l, n), 7.0, device="cuda")
+    api.fp8_linear_fwd(X, f, Y, ws)
+    assert api.averis_check_status(ws) == 0
+    w = R.deq(W.double().numpy(), (128, 128))
+    _check_product(Y[picks], R.deq(X[picks].double().cpu().numpy()), w.T, m)
+    rest = torch.ones(l, dtype=torch.bool, device="cuda")
+    rest[picks] = False
+    assert not Y[rest].any()
+    # the same rows as a buffer: row r of token t, scattered and gathered
+    row = torch.full((8, 1), -1, dtype=torch.int32, device="cuda")
+    cap = l // 128 * 128
+    row[: len(picks) - 1, 0] = torch.tensor(picks[:-1], dtype=torch.int32)
+    tokens, back = torch.randn(8, m, device="cuda").bfloat16(), torch.empty(8, m, dtype=torch.bfloat16, device="cuda")
+    api.moe_dispatch(tokens, row, X[:cap], ws)
+    api.moe_dispatch_bwd(X[:cap], row, back, ws)
+    assert api.averis_check_status(ws) == 0
+    assert torch.equal(back[: len(picks) - 1], tokens[: len(picks) - 1]) and not back[len(picks) - 1:].any()
+    xq = api.FP8Tensor(cap, m)
+    api.fp8_moe_dispatch(tokens, row, xq, ws)
+    q, s = R.quant(tokens.double().cpu().numpy())
+    got = R.e4m3_decode(xq.codes[picks[:-1]].cpu().numpy())
+    assert np.array_equal(got, q[: len(picks) - 1])
+    api.fp8_quant_t(X, api.FP8Tensor(m, -(-l // 128) * 128), ws)
+    assert api.averis_check_status(ws) == 0
