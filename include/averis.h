@@ -49,7 +49,8 @@
  *   - Shape rules: K (the contraction size) > 0 and K % 64 == 0; N % 64 == 0;
  *     l (tokens / rows) >= 0, any value (l = 0 is a no-op returning AVR_OK, and
  *     the tensor pointers may then be NULL);
- *     every pointer 16-byte aligned; l, K, N < 2^31.
+ *     every pointer 16-byte aligned; l, K, N < 2^31.  The routing calls and
+ *     the 8-bit linear layer state their own.
  */
 #ifndef AVERIS_H_
 #define AVERIS_H_
