@@ -484,23 +484,27 @@ def averis_split_quant_noalloc(X, rm, seed, offset, grad, mu, mu_q, xr_q, xr_deb
 # routing and 8-bit calls: the tensors are contiguous and on the current
 # device, else AverisError (invalid argument) before any launch
 # ---------------------------------------------------------------------------
-# the device and the stream as plain integers: torch.cuda.current_stream()
-# builds a Stream object, 3 us of a 4 us call
+# A decoding step's calls are bound by the host, so these wrappers take the
+# device and the stream as plain integers (torch.cuda.current_stream() builds
+# a Stream object, 3 us of a 5 us call), look at every tensor once and keep no
+# generic layer between.
 _device = getattr(torch._C, "_cuda_getDevice", None)               # absent from a torch without CUDA
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_DT = {torch.bfloat16: AVR_BF16, torch.float32: AVR_F32}
+_I32, _F32 = torch.int32, torch.float32
 
 
-def _call(name, stream, ws, *args, tensors=()):
+def _call(name, stream, ws, tensors, args):
     """The entry point with ws, its size and the stream appended."""
     dev = _device()
     for t in tensors:
-        if t is not None and not (t.get_device() == dev and t.is_contiguous()):
+        if t.get_device() != dev or not t.is_contiguous():
             _refuse_tensor(name, dev)
     if ws.get_device() != dev or not ws.is_contiguous():
         _refuse_tensor(name, dev)
     st = getattr(_LIB or load(), name)(*args, ws.data_ptr(), ws.nbytes,
                                        _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if st != AVR_OK:
+    if st:
         raise AverisError(st, name)
 
 
@@ -508,16 +512,32 @@ def _refuse_tensor(name, dev):
     raise AverisError(AVR_ERR_INVALID_ARG, f"{name}: every tensor must be contiguous and on device {dev}")
 
 
-def _shape(name, t, shape, dtype):
-    if t.shape != shape or t.dtype is not dtype:
-        raise AverisError(AVR_ERR_INVALID_ARG,
-                          f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+def _refuse_shape(name, *want):
+    """want: (tensor, shape, dtype) triples, one of which does not hold."""
+    for t, shape, dtype in want:
+        if t.shape != shape or t.dtype is not dtype:
+            raise AverisError(AVR_ERR_INVALID_ARG,
+                              f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    raise AverisError(AVR_ERR_INVALID_ARG, name)
+
+
+def _dt(t):
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {t.dtype}") from None
 
 
 def _route_workspace(n, device, stream):
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     averis_workspace_init(ws, stream)
     return ws
+
+
+def _positive(n, where):
+    if n == 0:
+        raise AverisError(AVR_ERR_UNSUPPORTED_SHAPE, where)
+    return n
 
 
 def moe_route_workspace_size(T, k, E):
@@ -529,12 +549,6 @@ def moe_route_workspace(T, k, E, device="cuda", stream=None):
     return _route_workspace(_positive(moe_route_workspace_size(T, k, E), "moe_route_workspace"), device, stream)
 
 
-def _positive(n, where):
-    if n == 0:
-        raise AverisError(AVR_ERR_UNSUPPORTED_SHAPE, where)
-    return n
-
-
 def moe_max_rows(T, k, E):
     """Rows of an experts' buffer that any routing of T tokens to k of E experts fits in."""
     return (T * k + 127 * min(E, T * k)) // 128 * 128
@@ -542,71 +556,79 @@ def moe_max_rows(T, k, E):
 
 def moe_route(logits, norm, ids, weights, ws, stream=None):
     T, E = logits.shape
-    k = ids.shape[1]
-    _shape("moe_route", ids, (T, k), torch.int32)
-    _shape("moe_route", weights, (T, k), torch.float32)
-    _call("moe_route", stream, ws, logits.data_ptr(), _dtype(logits), T, E, k, int(norm), ids.data_ptr(),
-          weights.data_ptr(), tensors=(logits, ids, weights))
+    iT, k = shape = ids.shape
+    if iT != T or ids.dtype is not _I32 or weights.shape != shape or weights.dtype is not _F32:
+        _refuse_shape("moe_route", (ids, (T, k), _I32), (weights, (T, k), _F32))
+    _call("moe_route", stream, ws, (logits, ids, weights),
+          (logits.data_ptr(), _dt(logits), T, E, k, 1 if norm else 0, ids.data_ptr(), weights.data_ptr()))
 
 
 def moe_route_bwd(logits, norm, ids, weights, dweights, dlogits, ws, stream=None):
     """logits may be None when norm is true."""
-    T, E = dlogits.shape
+    T, E = full = dlogits.shape
     k = ids.shape[1]
-    if logits is not None:
-        _shape("moe_route_bwd", logits, (T, E), dlogits.dtype)
-    _shape("moe_route_bwd", ids, (T, k), torch.int32)
-    _shape("moe_route_bwd", weights, (T, k), torch.float32)
-    _shape("moe_route_bwd", dweights, (T, k), torch.float32)
-    _call("moe_route_bwd", stream, ws, None if logits is None else logits.data_ptr(), _dtype(dlogits), T, E, k,
-          int(norm), ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(),
-          tensors=(logits, ids, weights, dweights, dlogits))
+    shape = (T, k)
+    if ids.shape != shape or ids.dtype is not _I32 or weights.shape != shape or weights.dtype is not _F32 \
+            or dweights.shape != shape or dweights.dtype is not _F32 \
+            or (logits is not None and (logits.shape != full or logits.dtype is not dlogits.dtype)):
+        _refuse_shape("moe_route_bwd", (ids, shape, _I32), (weights, shape, _F32), (dweights, shape, _F32),
+                      (dlogits if logits is None else logits, full, dlogits.dtype))
+    _call("moe_route_bwd", stream, ws,
+          (ids, weights, dweights, dlogits) + (() if logits is None else (logits,)),
+          (None if logits is None else logits.data_ptr(), _dt(dlogits), T, E, k, 1 if norm else 0, ids.data_ptr(),
+           weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr()))
 
 
 def moe_sort(ids, l_cap, counts, row, ws, stream=None):
-    T, k = ids.shape
-    _shape("moe_sort", ids, (T, k), torch.int32)
-    _shape("moe_sort", row, (T, k), torch.int32)
-    _shape("moe_sort", counts, (counts.numel(),), torch.int32)
-    _call("moe_sort", stream, ws, ids.data_ptr(), T, k, counts.numel(), l_cap, counts.data_ptr(), row.data_ptr(),
-          tensors=(ids, counts, row))
-
-
-def _permute_shapes(name, tokens, row, *bufs):
-    T, H = tokens.shape
-    k, l_cap = row.shape[1], bufs[0].shape[0]
-    _shape(name, row, (T, k), torch.int32)
-    for b in bufs:
-        _shape(name, b, (l_cap, H), tokens.dtype)
-    return T, k, H, l_cap
+    T, k = shape = ids.shape
+    if ids.dtype is not _I32 or row.shape != shape or row.dtype is not _I32 or counts.dtype is not _I32 \
+            or counts.dim() != 1:
+        _refuse_shape("moe_sort", (ids, shape, _I32), (row, shape, _I32), (counts, (counts.numel(),), _I32))
+    _call("moe_sort", stream, ws, (ids, counts, row),
+          (ids.data_ptr(), T, k, counts.shape[0], l_cap, counts.data_ptr(), row.data_ptr()))
 
 
 def moe_dispatch(X, row, Xp, ws, stream=None):
-    T, k, H, l_cap = _permute_shapes("moe_dispatch", X, row, Xp)
-    _call("moe_dispatch", stream, ws, X.data_ptr(), _dtype(X), T, k, H, row.data_ptr(), l_cap, Xp.data_ptr(),
-          tensors=(X, row, Xp))
+    T, H = X.shape
+    (rT, k), (l_cap, pH) = row.shape, Xp.shape
+    if rT != T or pH != H or row.dtype is not _I32 or Xp.dtype is not X.dtype:
+        _refuse_shape("moe_dispatch", (row, (T, k), _I32), (Xp, (l_cap, H), X.dtype))
+    _call("moe_dispatch", stream, ws, (X, row, Xp),
+          (X.data_ptr(), _dt(X), T, k, H, row.data_ptr(), l_cap, Xp.data_ptr()))
 
 
 def moe_dispatch_bwd(dXp, row, dX, ws, stream=None):
-    T, k, H, l_cap = _permute_shapes("moe_dispatch_bwd", dX, row, dXp)
-    _call("moe_dispatch_bwd", stream, ws, dXp.data_ptr(), _dtype(dX), T, k, H, row.data_ptr(), l_cap, dX.data_ptr(),
-          tensors=(dXp, row, dX))
+    T, H = dX.shape
+    (rT, k), (l_cap, pH) = row.shape, dXp.shape
+    if rT != T or pH != H or row.dtype is not _I32 or dXp.dtype is not dX.dtype:
+        _refuse_shape("moe_dispatch_bwd", (row, (T, k), _I32), (dXp, (l_cap, H), dX.dtype))
+    _call("moe_dispatch_bwd", stream, ws, (dXp, row, dX),
+          (dXp.data_ptr(), _dt(dX), T, k, H, row.data_ptr(), l_cap, dX.data_ptr()))
 
 
 def moe_combine(Yp, row, weights, Y, ws, stream=None):
-    T, k, H, l_cap = _permute_shapes("moe_combine", Y, row, Yp)
-    _shape("moe_combine", weights, (T, k), torch.float32)
-    _call("moe_combine", stream, ws, Yp.data_ptr(), _dtype(Y), T, k, H, row.data_ptr(), weights.data_ptr(), l_cap,
-          Y.data_ptr(), tensors=(Yp, row, weights, Y))
+    T, H = Y.shape
+    T_k = rT, k = row.shape
+    l_cap, pH = Yp.shape
+    if rT != T or pH != H or row.dtype is not _I32 or weights.shape != T_k or weights.dtype is not _F32 \
+            or Yp.dtype is not Y.dtype:
+        _refuse_shape("moe_combine", (row, (T, k), _I32), (weights, (T, k), _F32), (Yp, (l_cap, H), Y.dtype))
+    _call("moe_combine", stream, ws, (Yp, row, weights, Y),
+          (Yp.data_ptr(), _dt(Y), T, k, H, row.data_ptr(), weights.data_ptr(), l_cap, Y.data_ptr()))
 
 
 def moe_combine_bwd(dY, Yp, row, weights, dYp, dweights, ws, stream=None):
-    T, k, H, l_cap = _permute_shapes("moe_combine_bwd", dY, row, Yp, dYp)
-    _shape("moe_combine_bwd", weights, (T, k), torch.float32)
-    _shape("moe_combine_bwd", dweights, (T, k), torch.float32)
-    _call("moe_combine_bwd", stream, ws, dY.data_ptr(), Yp.data_ptr(), _dtype(dY), T, k, H, row.data_ptr(),
-          weights.data_ptr(), l_cap, dYp.data_ptr(), dweights.data_ptr(),
-          tensors=(dY, Yp, row, weights, dYp, dweights))
+    T, H = dY.shape
+    T_k = rT, k = row.shape
+    buf = l_cap, pH = Yp.shape
+    if rT != T or pH != H or row.dtype is not _I32 or weights.shape != T_k or weights.dtype is not _F32 \
+            or dweights.shape != T_k or dweights.dtype is not _F32 or Yp.dtype is not dY.dtype \
+            or dYp.shape != buf or dYp.dtype is not dY.dtype:
+        _refuse_shape("moe_combine_bwd", (row, (T, k), _I32), (weights, (T, k), _F32), (dweights, (T, k), _F32),
+                      (Yp, (l_cap, H), dY.dtype), (dYp, (l_cap, H), dY.dtype))
+    _call("moe_combine_bwd", stream, ws, (dY, Yp, row, weights, dYp, dweights),
+          (dY.data_ptr(), Yp.data_ptr(), _dt(dY), T, k, H, row.data_ptr(), weights.data_ptr(), l_cap,
+           dYp.data_ptr(), dweights.data_ptr()))
 
 
 class FP8Tensor:
@@ -617,27 +639,42 @@ class FP8Tensor:
         n = avr_fp8_scales_bytes(rows, K)
         if rows > 0:
             _positive(n, "FP8Tensor")
-        self.rows, self.K = int(rows), int(K)
-        self.codes = torch.empty((self.rows, self.K), dtype=torch.uint8, device=device)
-        self.scales = torch.empty(n, dtype=torch.uint8, device=device)
+        self._hold(torch.empty((int(rows), int(K)), dtype=torch.uint8, device=device),
+                   torch.empty(n, dtype=torch.uint8, device=device))
 
     @classmethod
     def of(cls, codes, scales):
         """The tensor held by codes [rows, K] and scales (uint8, not copied)."""
-        t = cls.__new__(cls)
-        t.rows, t.K = codes.shape
+        rows, K = codes.shape
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 \
-                or scales.numel() != avr_fp8_scales_bytes(t.rows, t.K):
+                or scales.numel() != avr_fp8_scales_bytes(rows, K):
             raise AverisError(AVR_ERR_INVALID_ARG, "FP8Tensor.of")
-        t.codes, t.scales = codes, scales
+        t = cls.__new__(cls)
+        t._hold(codes, scales)
         return t
 
+    def _hold(self, codes, scales):
+        self._parts = (codes, scales)
+        self._c = avr_fp8(0, 0, codes.shape[0], codes.shape[1])
+        self._ref = ctypes.byref(self._c)
+
+    codes = property(lambda self: self._parts[0])
+    scales = property(lambda self: self._parts[1])
+    rows = property(lambda self: self._c.rows)
+    K = property(lambda self: self._c.K)
+
     def struct(self):
-        return avr_fp8(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.K)
+        c, (codes, scales) = self._c, self._parts
+        c.codes, c.scales = codes.data_ptr(), scales.data_ptr()
+        return c
 
 
 def _q(t):
-    return (None, ()) if t is None else (ctypes.byref(t.struct()), (t.codes, t.scales))
+    """(a reference to the descriptor, its tensors) of an FP8Tensor or None."""
+    if t is None:
+        return None, ()
+    t.struct()
+    return t._ref, t._parts
 
 
 def avr_fp8_scales_bytes(rows, K):
@@ -656,52 +693,52 @@ def fp8_workspace(l, m, n, device="cuda", stream=None):
 def fp8_quant(X, out, ws, stream=None):
     rows, K = X.shape
     q, t = _q(out)
-    _call("fp8_quant", stream, ws, X.data_ptr(), _dtype(X), rows, K, q, tensors=(X,) + t)
+    _call("fp8_quant", stream, ws, (X,) + t, (X.data_ptr(), _dt(X), rows, K, q))
 
 
 def fp8_quant_t(X, out, ws, stream=None):
     """out: FP8Tensor(K, l rounded up to 128)."""
     l, K = X.shape
     q, t = _q(out)
-    _call("fp8_quant_t", stream, ws, X.data_ptr(), _dtype(X), l, K, q, tensors=(X,) + t)
+    _call("fp8_quant_t", stream, ws, (X,) + t, (X.data_ptr(), _dt(X), l, K, q))
 
 
 def fp8_quant_weight(W, w_fwd, w_dgrad, ws, stream=None):
     """w_dgrad may be None."""
     m, n = W.shape
     (f, tf), (d, td) = _q(w_fwd), _q(w_dgrad)
-    _call("fp8_quant_weight", stream, ws, W.data_ptr(), _dtype(W), m, n, f, d, tensors=(W,) + tf + td)
+    _call("fp8_quant_weight", stream, ws, (W,) + tf + td, (W.data_ptr(), _dt(W), m, n, f, d))
 
 
 def fp8_gemm(a, b, Y, ws, stream=None):
     (qa, ta), (qb, tb) = _q(a), _q(b)
-    _shape("fp8_gemm", Y, (a.rows, b.rows), Y.dtype)
-    _call("fp8_gemm", stream, ws, qa, qb, Y.data_ptr(), _dtype(Y), tensors=(Y,) + ta + tb)
+    if Y.shape != (a.rows, b.rows):
+        _refuse_shape("fp8_gemm", (Y, (a.rows, b.rows), Y.dtype))
+    _call("fp8_gemm", stream, ws, (Y,) + ta + tb, (qa, qb, Y.data_ptr(), _dt(Y)))
 
 
 def fp8_linear_fwd(X, w_fwd, Y, ws, stream=None):
-    l, m = X.shape
-    q, t = _q(w_fwd)
-    _shape("fp8_linear_fwd", Y, (l, w_fwd.rows), Y.dtype)
-    _call("fp8_linear_fwd", stream, ws, X.data_ptr(), _dtype(X), l, m, w_fwd.rows, q, Y.data_ptr(), _dtype(Y),
-          tensors=(X, Y) + t)
+    (l, m), (q, t) = X.shape, _q(w_fwd)
+    n = w_fwd.rows
+    if Y.shape != (l, n):
+        _refuse_shape("fp8_linear_fwd", (Y, (l, n), Y.dtype))
+    _call("fp8_linear_fwd", stream, ws, (X, Y) + t, (X.data_ptr(), _dt(X), l, m, n, q, Y.data_ptr(), _dt(Y)))
 
 
 def fp8_linear_dgrad(D, w_dgrad, dX, ws, stream=None):
-    l, n = D.shape
-    q, t = _q(w_dgrad)
-    _shape("fp8_linear_dgrad", dX, (l, w_dgrad.rows), dX.dtype)
-    _call("fp8_linear_dgrad", stream, ws, D.data_ptr(), _dtype(D), l, w_dgrad.rows, n, q, dX.data_ptr(), _dtype(dX),
-          tensors=(D, dX) + t)
+    (l, n), (q, t) = D.shape, _q(w_dgrad)
+    m = w_dgrad.rows
+    if dX.shape != (l, m):
+        _refuse_shape("fp8_linear_dgrad", (dX, (l, m), dX.dtype))
+    _call("fp8_linear_dgrad", stream, ws, (D, dX) + t, (D.data_ptr(), _dt(D), l, m, n, q, dX.data_ptr(), _dt(dX)))
 
 
 def fp8_linear_wgrad(X, D, dW, ws, stream=None):
-    l, m = X.shape
-    n = D.shape[1]
-    _shape("fp8_linear_wgrad", D, (l, n), D.dtype)
-    _shape("fp8_linear_wgrad", dW, (m, n), dW.dtype)
-    _call("fp8_linear_wgrad", stream, ws, X.data_ptr(), _dtype(X), D.data_ptr(), _dtype(D), l, m, n, dW.data_ptr(),
-          _dtype(dW), tensors=(X, D, dW))
+    (l, m), (dl, n) = X.shape, D.shape
+    if dl != l or dW.shape != (m, n):
+        _refuse_shape("fp8_linear_wgrad", (D, (l, n), D.dtype), (dW, (m, n), dW.dtype))
+    _call("fp8_linear_wgrad", stream, ws, (X, D, dW),
+          (X.data_ptr(), _dt(X), D.data_ptr(), _dt(D), l, m, n, dW.data_ptr(), _dt(dW)))
 
 
 def fp8_moe_workspace_size(l_cap, m, n, E):
@@ -719,53 +756,47 @@ def fp8_moe_quant_weights(W, w_fwd, w_dgrad, ws, stream=None):
     """w_dgrad may be None."""
     E, m, n = W.shape
     (f, tf), (d, td) = _q(w_fwd), _q(w_dgrad)
-    _call("fp8_moe_quant_weights", stream, ws, W.data_ptr(), _dtype(W), E, m, n, f, d, tensors=(W,) + tf + td)
+    _call("fp8_moe_quant_weights", stream, ws, (W,) + tf + td, (W.data_ptr(), _dt(W), E, m, n, f, d))
 
 
 def fp8_moe_dispatch(X, row, xq, ws, stream=None):
-    T, K = X.shape
-    k = row.shape[1]
-    q, t = _q(xq)
-    _shape("fp8_moe_dispatch", row, (T, k), torch.int32)
-    _call("fp8_moe_dispatch", stream, ws, X.data_ptr(), _dtype(X), T, k, K, row.data_ptr(), q, tensors=(X, row) + t)
+    (T, K), (rT, k), (q, t) = X.shape, row.shape, _q(xq)
+    if rT != T or row.dtype is not _I32:
+        _refuse_shape("fp8_moe_dispatch", (row, (T, k), _I32))
+    _call("fp8_moe_dispatch", stream, ws, (X, row) + t, (X.data_ptr(), _dt(X), T, k, K, row.data_ptr(), q))
 
 
 def fp8_moe_gemm(xq, counts, w, Y, ws, stream=None):
     (qx, tx), (qw, tw) = _q(xq), _q(w)
     E = counts.numel()
-    _shape("fp8_moe_gemm", counts, (E,), torch.int32)
-    _shape("fp8_moe_gemm", Y, (xq.rows, w.rows // max(E, 1)), Y.dtype)
-    _call("fp8_moe_gemm", stream, ws, qx, counts.data_ptr(), E, qw, Y.data_ptr(), _dtype(Y),
-          tensors=(counts, Y) + tx + tw)
-
-
-def _moe_shapes(name, X, counts, w, Y):
-    l_cap, E = X.shape[0], counts.numel()
-    _shape(name, counts, (E,), torch.int32)
-    N = w.rows // max(E, 1)
-    _shape(name, Y, (l_cap, N), Y.dtype)
-    return l_cap, E, X.shape[1], N
+    want = (xq.rows, w.rows // (E or 1))
+    if counts.dtype is not _I32 or Y.shape != want:
+        _refuse_shape("fp8_moe_gemm", (counts, counts.shape, _I32), (Y, want, Y.dtype))
+    _call("fp8_moe_gemm", stream, ws, (counts, Y) + tx + tw, (qx, counts.data_ptr(), E, qw, Y.data_ptr(), _dt(Y)))
 
 
 def fp8_moe_linear_fwd(X, counts, w_fwd, Y, ws, stream=None):
-    l_cap, E, m, n = _moe_shapes("fp8_moe_linear_fwd", X, counts, w_fwd, Y)
-    q, t = _q(w_fwd)
-    _call("fp8_moe_linear_fwd", stream, ws, X.data_ptr(), _dtype(X), l_cap, counts.data_ptr(), E, m, n, q,
-          Y.data_ptr(), _dtype(Y), tensors=(X, counts, Y) + t)
+    (l_cap, m), E, (q, t) = X.shape, counts.numel(), _q(w_fwd)
+    n = w_fwd.rows // (E or 1)
+    if counts.dtype is not _I32 or Y.shape != (l_cap, n):
+        _refuse_shape("fp8_moe_linear_fwd", (counts, counts.shape, _I32), (Y, (l_cap, n), Y.dtype))
+    _call("fp8_moe_linear_fwd", stream, ws, (X, counts, Y) + t,
+          (X.data_ptr(), _dt(X), l_cap, counts.data_ptr(), E, m, n, q, Y.data_ptr(), _dt(Y)))
 
 
 def fp8_moe_linear_dgrad(D, counts, w_dgrad, dX, ws, stream=None):
-    l_cap, E, n, m = _moe_shapes("fp8_moe_linear_dgrad", D, counts, w_dgrad, dX)
-    q, t = _q(w_dgrad)
-    _call("fp8_moe_linear_dgrad", stream, ws, D.data_ptr(), _dtype(D), l_cap, counts.data_ptr(), E, m, n, q,
-          dX.data_ptr(), _dtype(dX), tensors=(D, counts, dX) + t)
+    (l_cap, n), E, (q, t) = D.shape, counts.numel(), _q(w_dgrad)
+    m = w_dgrad.rows // (E or 1)
+    if counts.dtype is not _I32 or dX.shape != (l_cap, m):
+        _refuse_shape("fp8_moe_linear_dgrad", (counts, counts.shape, _I32), (dX, (l_cap, m), dX.dtype))
+    _call("fp8_moe_linear_dgrad", stream, ws, (D, counts, dX) + t,
+          (D.data_ptr(), _dt(D), l_cap, counts.data_ptr(), E, m, n, q, dX.data_ptr(), _dt(dX)))
 
 
 def fp8_moe_linear_wgrad(X, D, counts, dW, ws, stream=None):
-    l_cap, m = X.shape
-    n, E = D.shape[1], counts.numel()
-    _shape("fp8_moe_linear_wgrad", D, (l_cap, n), D.dtype)
-    _shape("fp8_moe_linear_wgrad", counts, (E,), torch.int32)
-    _shape("fp8_moe_linear_wgrad", dW, (E, m, n), dW.dtype)
-    _call("fp8_moe_linear_wgrad", stream, ws, X.data_ptr(), _dtype(X), D.data_ptr(), _dtype(D), l_cap,
-          counts.data_ptr(), E, m, n, dW.data_ptr(), _dtype(dW), tensors=(X, D, counts, dW))
+    (l_cap, m), (dl, n), E = X.shape, D.shape, counts.numel()
+    if dl != l_cap or counts.dtype is not _I32 or dW.shape != (E, m, n):
+        _refuse_shape("fp8_moe_linear_wgrad", (D, (l_cap, n), D.dtype), (counts, counts.shape, _I32),
+                      (dW, (E, m, n), dW.dtype))
+    _call("fp8_moe_linear_wgrad", stream, ws, (X, D, counts, dW),
+          (X.data_ptr(), _dt(X), D.data_ptr(), _dt(D), l_cap, counts.data_ptr(), E, m, n, dW.data_ptr(), _dt(dW)))
