@@ -71,9 +71,86 @@ __device__ __forceinline__ uint4 pack(const float (&f)[Vec<kBf16>::kN]) {
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// router: one warp per token, expert lane + 32 i in register i of a lane
+// router: one warp per token, experts NV lane .. NV lane + NV - 1 in a lane's
+// registers, so that a lower lane holds lower experts
 // ---------------------------------------------------------------------------
 constexpr int kRouteWarps = 4;
+
+// the NV values of a lane from e0 on, -inf past E; wide: rows can be read and
+// written min(NV, 4) values at a time
+template <bool kBf16, int NV>
+__device__ __forceinline__ void load_lane(const void* row, int e0, int E, bool wide, float (&v)[NV]) {
+  constexpr int W = NV < 4 ? NV : 4;
+  if (wide && W > 1) {
+#pragma unroll
+    for (int i = 0; i < NV; i += W) {
+      uint32_t w[4] = {};
+      const bool in = e0 + i < E;
+      if (kBf16) {
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(row) + e0 + i;
+        if (in && W == 4) {
+          const uint2 x = *reinterpret_cast<const uint2*>(p);
+          w[0] = x.x << 16, w[1] = x.x & 0xFFFF0000u, w[2] = x.y << 16, w[3] = x.y & 0xFFFF0000u;
+        } else if (in) {
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+          w[0] = x << 16, w[1] = x & 0xFFFF0000u;
+        }
+      } else {
+        const float* p = static_cast<const float*>(row) + e0 + i;
+        if (in && W == 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p);
+          w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else if (in) {
+          const uint2 x = *reinterpret_cast<const uint2*>(p);
+          w[0] = x.x, w[1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < W; ++c) v[i + c] = in ? __uint_as_float(w[c]) : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = e0 + i < E ? load1<kBf16>(row, e0 + i) : -INFINITY;
+  }
+}
+template <bool kBf16, int NV>
+__device__ __forceinline__ void store_lane(void* row, int e0, int E, bool wide, const float (&v)[NV]) {
+  constexpr int W = NV < 4 ? NV : 4;
+  if (wide && W > 1) {
+#pragma unroll
+    for (int i = 0; i < NV; i += W) {
+      if (e0 + i >= E) continue;
+      if (kBf16) {
+        uint32_t w[W / 2 > 0 ? W / 2 : 1];
+#pragma unroll
+        for (int c = 0; c < W / 2; ++c) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * c], v[i + 2 * c + 1]);
+          w[c] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(row) + e0 + i;
+        if (W == 4)
+          *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[W / 2 - 1]);
+        else
+          *reinterpret_cast<uint32_t*>(p) = w[0];
+      } else {
+        float* p = static_cast<float*>(row) + e0 + i;
+        if (W == 4)
+          *reinterpret_cast<float4*>(p) = make_float4(v[i], v[i + 1], v[i + W - 2], v[i + W - 1]);
+        else
+          *reinterpret_cast<float2*>(p) = make_float2(v[i], v[i + W - 1]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (e0 + i < E) store1<kBf16>(row, e0 + i, v[i]);
+  }
+}
+template <bool kBf16>
+__device__ __forceinline__ const void* row_of(const void* p, int64_t at) {
+  return kBf16 ? static_cast<const void*>(static_cast<const __nv_bfloat16*>(p) + at)
+               : static_cast<const void*>(static_cast<const float*>(p) + at);
+}
 
 // a key that orders as the value does, above 0 for every value but -inf (and
 // NaN); + 0.0f makes the two zeros one value
@@ -92,12 +169,16 @@ __device__ __forceinline__ float key_value(uint32_t u) {
 // instructions (the logits are 17 MB for 32768 tokens of 128 experts), so a
 // step is kept short: a lane sorts its keys once (descending, the lower expert
 // first among equal ones; for up to 8, beyond that it searches), its best is
-// always the first, and the lane that holds the step's maximum notes its
-// expert in shared memory and moves up by one.  Lanes that tie, which is rare,
-// settle it by a second reduction.
+// always the first, and the lowest lane that holds the step's maximum notes its
+// expert in shared memory and moves up by one.  A lane's experts are
+// neighbours, so its row comes in one wide load and ties need no second
+// reduction: 32768 tokens of 128 experts, 8 slots, take 14.8 us (13.9 with
+// `norm`), with experts 32 apart and a vote on ties 16.7 (15.7); 256 experts
+// 27.0 against 29.6.  The gradient of the same tokens: 12.4 us.
 template <bool kBf16, int NV>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const void* logits, int64_t T, int E, int k, int norm,
-                                                                 int32_t* ids, float* weights, uint32_t* status) {
+                                                                 bool wide, int32_t* ids, float* weights,
+                                                                 uint32_t* status) {
   __shared__ int32_t s_slot[kRouteWarps][kMaxSlots];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
@@ -105,14 +186,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const void* log
   int32_t* slot = s_slot[threadIdx.x >> 5];
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (t >= T) return;
+  const int e0 = NV * lane;
   float v[NV];
   uint32_t key[NV];
   bool bad = false;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
-    v[i] = e < E ? load1<kBf16>(logits, t * E + e) : -INFINITY;
-  }
+  load_lane<kBf16, NV>(row_of<kBf16>(logits, t * E), e0, E, wide, v);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     bad |= !(v[i] < INFINITY);
@@ -166,13 +244,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const void* log
     }
     const uint32_t m = __reduce_max_sync(kFull, best);
     if (m == 0u) break;               // only -inf left
-    const uint32_t e = lane + 32u * best_at;
-    bool mine = best == m;
-    const uint32_t tie = __ballot_sync(kFull, mine);
-    if (tie & (tie - 1u)) mine = e == __reduce_min_sync(kFull, mine ? e : 0xFFFFFFFFu);
+    const bool mine = __ffs(__ballot_sync(kFull, best == m)) == lane + 1;
     if (lane == taken) my_key = m;
     if (mine) {
-      slot[taken] = static_cast<int32_t>(e);
+      slot[taken] = e0 + static_cast<int32_t>(best_at);
       if (kSort) {
         order >>= 4;
 #pragma unroll
@@ -205,23 +280,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const void* log
 // row of shared memory, so the logits' loop needs no search.
 template <bool kBf16, int NV>
 __global__ void __launch_bounds__(32 * kRouteWarps)
-    route_bwd_kernel(const void* logits, int64_t T, int E, int k, int norm, const int32_t* ids, const float* weights,
-                     const float* dweights, void* dlogits, uint32_t* status) {
-  __shared__ float s_row[kRouteWarps][32 * NV];
+    route_bwd_kernel(const void* logits, int64_t T, int E, int k, int norm, bool wide, const int32_t* ids,
+                     const float* weights, const float* dweights, void* dlogits, uint32_t* status) {
+  __shared__ __align__(16) float s_row[kRouteWarps][32 * NV];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int lane = threadIdx.x & 31;
   float* row = s_row[threadIdx.x >> 5];
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (t >= T) return;
+  const int e0 = NV * lane;
   float v[NV];
-  if (!norm) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
-      v[i] = e < E ? load1<kBf16>(logits, t * E + e) : -INFINITY;
-    }
-  }
+  if (!norm) load_lane<kBf16, NV>(row_of<kBf16>(logits, t * E), e0, E, wide, v);
   int id = -1;
   float w = 0.0f, dw = 0.0f;
   if (lane < k) {
@@ -237,7 +307,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   }
   const float s = warp_sum(w * dw);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) row[lane + 32 * i] = 0.0f;
+  for (int i = 0; i < NV; ++i) row[e0 + i] = 0.0f;
   __syncwarp();
   // every slot leaves its number at its expert; a slot that finds another's
   // there shares the expert with it (a row that names one twice)
@@ -254,10 +324,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
       __syncwarp();
     }
   }
-  if (norm) {
+  float d[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (lane + 32 * i < E) store1<kBf16>(dlogits, t * E + lane + 32 * i, row[lane + 32 * i]);
+  for (int i = 0; i < NV; ++i) d[i] = row[e0 + i];
+  void* out = const_cast<void*>(row_of<kBf16>(dlogits, t * E));
+  if (norm) {
+    store_lane<kBf16, NV>(out, e0, E, wide, d);
     return;
   }
   float top = -INFINITY, den = 0.0f;
@@ -273,19 +345,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   den = warp_sum(den);
   const float c = den > 0.0f ? s / den : 0.0f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (lane + 32 * i < E) store1<kBf16>(dlogits, t * E + lane + 32 * i, row[lane + 32 * i] - v[i] * c);
+  for (int i = 0; i < NV; ++i) d[i] -= v[i] * c;
+  store_lane<kBf16, NV>(out, e0, E, wide, d);
 }
 
 template <bool kBf16, int NV>
 static cudaError_t route_t(const void* logits, int64_t T, int E, int k, int norm, int32_t* ids, float* weights,
                            const float* dweights, void* dlogits, uint32_t* status, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((T + kRouteWarps - 1) / kRouteWarps));
+  const bool wide = E % (NV < 4 ? NV : 4) == 0;        // the tensors start on 16 bytes
   if (dlogits == nullptr)
-    return launch_ex(route_kernel<kBf16, NV>, grid, dim3(32 * kRouteWarps), 0, s, true, logits, T, E, k, norm, ids,
-                     weights, status);
-  return launch_ex(route_bwd_kernel<kBf16, NV>, grid, dim3(32 * kRouteWarps), 0, s, true, logits, T, E, k, norm, ids,
-                   weights, dweights, dlogits, status);
+    return launch_ex(route_kernel<kBf16, NV>, grid, dim3(32 * kRouteWarps), 0, s, true, logits, T, E, k, norm,
+                     wide, ids, weights, status);
+  return launch_ex(route_bwd_kernel<kBf16, NV>, grid, dim3(32 * kRouteWarps), 0, s, true, logits, T, E, k, norm,
+                   wide, ids, weights, dweights, dlogits, status);
 }
 
 template <bool kBf16>

@@ -62,6 +62,31 @@ def test_route_matches_the_definition(api, T, E, k, dt, norm):
     assert np.all(np.abs(w.cpu().numpy().astype(np.float64) - rw) <= _weight_tol(l, rw, E))
 
 
+@pytest.mark.parametrize("E", [30, 34, 63, 65, 98, 100, 127, 130, 200, 252, 257, 300, 511, 514, 1000, 1023])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_route_every_width_with_ties_and_gradient(api, E, dt):
+    """Rows that can and cannot be read several values at a time, whose end
+    falls inside a lane's experts, ties between lanes and inside one."""
+    T, k = 21, 9
+    lt = _logits(T, E, dt, E, ties=True)
+    lt[::4, E // 2:] = float("-inf")
+    l = lt.double().numpy()
+    ids, w, ws = _route(api, lt, k, False)
+    rid, rw = R.route(l, k, False)
+    assert api.averis_check_status(ws) == 0
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    assert np.all(np.abs(w.cpu().numpy().astype(np.float64) - rw) <= _weight_tol(l, rw, E))
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(E)).cuda()
+    dl = torch.full((T, E), 9.0, dtype=DT[dt], device="cuda")
+    api.moe_route_bwd(lt.cuda(), False, ids, w, dw, dl, ws)
+    wn, dn = w.cpu().numpy(), dw.cpu().numpy()
+    ref = R.route_bwd(l, False, rid, wn, dn)
+    # as in test_route_gradient_matches_the_formula
+    mag = np.abs(wn).max(1, keepdims=True) * (np.abs(dn).max(1, keepdims=True) * (1 + k))
+    tol = mag * ((2 * k + E + 80) * 2.0 ** -24) + EPS[DT[dt]] * np.abs(ref)
+    assert np.all(np.abs(dl.double().cpu().numpy() - ref) <= tol)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_route_ties_go_to_the_lower_expert(api, dt):
     lt = _logits(200, 96, dt, 5, ties=True)
