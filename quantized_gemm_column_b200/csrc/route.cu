@@ -74,7 +74,13 @@ __device__ __forceinline__ uint4 pack(const float (&f)[Vec<kBf16>::kN]) {
 // router: one warp per token, experts NV lane .. NV lane + NV - 1 in a lane's
 // registers, so that a lower lane holds lower experts
 // ---------------------------------------------------------------------------
-constexpr int kRouteWarps = 4;
+// Warps of a block.  A GPU starts about one block in a nanosecond, which with
+// 4 warps is all the time that many tokens of few experts take: the gradient
+// of 32768 tokens of 128 experts with `norm` takes 5.2 us with 8 and 8.9 with
+// 4 (12: 5.1), the router's 16 experts 7.7 and 9.0.  Beyond 128 experts a
+// token works longer and larger blocks end unevenly: 4096 tokens of 256
+// experts 5.4 with 8, 5.0 with 4.
+__host__ __device__ constexpr int route_warps(int nv) { return nv <= 4 ? 8 : 4; }
 
 // the NV values of a lane from e0 on, -inf past E; wide: rows can be read and
 // written min(NV, 4) values at a time
@@ -172,19 +178,20 @@ __device__ __forceinline__ float key_value(uint32_t u) {
 // always the first, and the lowest lane that holds the step's maximum notes its
 // expert in shared memory and moves up by one.  A lane's experts are
 // neighbours, so its row comes in one wide load and ties need no second
-// reduction: 32768 tokens of 128 experts, 8 slots, take 14.8 us (13.9 with
+// reduction: 32768 tokens of 128 experts, 8 slots, take 14.9 us (13.9 with
 // `norm`), with experts 32 apart and a vote on ties 16.7 (15.7); 256 experts
-// 27.0 against 29.6.  The gradient of the same tokens: 12.4 us.
+// 27.0 against 29.6.  The gradient of the
+// 128 experts' tokens takes 9.5 us (5.4 with `norm`, which reads no logits).
 template <bool kBf16, int NV>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const void* logits, int64_t T, int E, int k, int norm,
+__global__ void __launch_bounds__(32 * route_warps(NV)) route_kernel(const void* logits, int64_t T, int E, int k, int norm,
                                                                  bool wide, int32_t* ids, float* weights,
                                                                  uint32_t* status) {
-  __shared__ int32_t s_slot[kRouteWarps][kMaxSlots];
+  __shared__ int32_t s_slot[route_warps(NV)][kMaxSlots];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int lane = threadIdx.x & 31;
   int32_t* slot = s_slot[threadIdx.x >> 5];
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * route_warps(NV) + (threadIdx.x >> 5);
   if (t >= T) return;
   const int e0 = NV * lane;
   float v[NV];
@@ -279,33 +286,49 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const void* log
 // Gradient: lane j holds slot j; the chosen experts' terms are added into a
 // row of shared memory, so the logits' loop needs no search.
 template <bool kBf16, int NV>
-__global__ void __launch_bounds__(32 * kRouteWarps)
+__global__ void __launch_bounds__(32 * route_warps(NV))
     route_bwd_kernel(const void* logits, int64_t T, int E, int k, int norm, bool wide, const int32_t* ids,
                      const float* weights, const float* dweights, void* dlogits, uint32_t* status) {
-  __shared__ __align__(16) float s_row[kRouteWarps][32 * NV];
+  __shared__ __align__(16) float s_row[route_warps(NV)][32 * NV];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int lane = threadIdx.x & 31;
   float* row = s_row[threadIdx.x >> 5];
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * route_warps(NV) + (threadIdx.x >> 5);
   if (t >= T) return;
   const int e0 = NV * lane;
   float v[NV];
   if (!norm) load_lane<kBf16, NV>(row_of<kBf16>(logits, t * E), e0, E, wide, v);
   int id = -1;
   float w = 0.0f, dw = 0.0f;
-  if (lane < k) {
+  if (lane < k) {                     // the three loads in flight together; an empty slot's values are not used
     id = ids[t * k + lane];
+    w = weights[t * k + lane];
+    dw = dweights[t * k + lane];
     if (id >= E) {
       raise_status(status, AVR_ERR_INVALID_ARG);
       id = -1;
     }
-    if (id >= 0) {
-      w = weights[t * k + lane];
-      dw = dweights[t * k + lane];
+    if (id < 0) w = dw = 0.0f;
+  }
+  float s = w * dw, den = 0.0f;
+  if (!norm) {
+    uint32_t top_key = 0u;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) top_key = max(top_key, order_key(v[i]));
+    top_key = __reduce_max_sync(kFull, top_key);
+    const float top = key_value(top_key);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v[i] = top_key != 0u ? expf(v[i] - top) : 0.0f;       // 0: every logit is -inf
+      den += v[i];
     }
   }
-  const float s = warp_sum(w * dw);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {  // both sums, one chain of shuffles
+    s += __shfl_xor_sync(kFull, s, o);
+    den += __shfl_xor_sync(kFull, den, o);
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) row[e0 + i] = 0.0f;
   __syncwarp();
@@ -332,17 +355,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     store_lane<kBf16, NV>(out, e0, E, wide, d);
     return;
   }
-  float top = -INFINITY, den = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) top = fmaxf(top, v[i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    v[i] = top > -INFINITY ? expf(v[i] - top) : 0.0f;
-    den += v[i];
-  }
-  den = warp_sum(den);
   const float c = den > 0.0f ? s / den : 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) d[i] -= v[i] * c;
@@ -352,12 +364,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 template <bool kBf16, int NV>
 static cudaError_t route_t(const void* logits, int64_t T, int E, int k, int norm, int32_t* ids, float* weights,
                            const float* dweights, void* dlogits, uint32_t* status, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((T + kRouteWarps - 1) / kRouteWarps));
+  constexpr int kWarps = route_warps(NV);
+  const dim3 grid(static_cast<unsigned>((T + kWarps - 1) / kWarps));
   const bool wide = E % (NV < 4 ? NV : 4) == 0;        // the tensors start on 16 bytes
   if (dlogits == nullptr)
-    return launch_ex(route_kernel<kBf16, NV>, grid, dim3(32 * kRouteWarps), 0, s, true, logits, T, E, k, norm,
+    return launch_ex(route_kernel<kBf16, NV>, grid, dim3(32 * kWarps), 0, s, true, logits, T, E, k, norm,
                      wide, ids, weights, status);
-  return launch_ex(route_bwd_kernel<kBf16, NV>, grid, dim3(32 * kRouteWarps), 0, s, true, logits, T, E, k, norm,
+  return launch_ex(route_bwd_kernel<kBf16, NV>, grid, dim3(32 * kWarps), 0, s, true, logits, T, E, k, norm,
                    wide, ids, weights, dweights, dlogits, status);
 }
 
