@@ -180,12 +180,12 @@ __device__ __forceinline__ float key_value(uint32_t u) {
 // neighbours, so its row comes in one wide load and ties need no second
 // reduction: 32768 tokens of 128 experts, 8 slots, take 14.9 us (13.9 with
 // `norm`), with experts 32 apart and a vote on ties 16.7 (15.7); 256 experts
-// 27.0 against 29.6.  The gradient of the
-// 128 experts' tokens takes 9.5 us (5.4 with `norm`, which reads no logits).
+// 27.0 against 29.6.  The gradient of the 128 experts' tokens takes 9.5 us (5.4
+// with `norm`, which reads no logits).
 template <bool kBf16, int NV>
-__global__ void __launch_bounds__(32 * route_warps(NV)) route_kernel(const void* logits, int64_t T, int E, int k, int norm,
-                                                                 bool wide, int32_t* ids, float* weights,
-                                                                 uint32_t* status) {
+__global__ void __launch_bounds__(32 * route_warps(NV))
+    route_kernel(const void* logits, int64_t T, int E, int k, int norm, bool wide, int32_t* ids, float* weights,
+                 uint32_t* status) {
   __shared__ int32_t s_slot[route_warps(NV)][kMaxSlots];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
