@@ -579,8 +579,14 @@ __device__ __forceinline__ int64_t slot_row(const PermuteArgs& a, int64_t t, int
   return r;
 }
 
-constexpr int kDispU = 4;
+// With few tokens (T times the 16-byte vectors of a row up to this) a strip is
+// one vector a lane, so that the work spreads over four times the warps and
+// all of a token's loads are in flight together: 64 tokens of 2048 bf16, 8
+// slots, dispatch 1.8 us against 2.3 and combine 3.2 against 3.5; 512 tokens
+// 3.8 and 5.4 against 3.7 and 4.2.
+constexpr int64_t kFewVectors = 32768;
 
+template <int kU>
 __global__ void __launch_bounds__(kPermThreads) dispatch_kernel(const PermuteArgs a, int64_t V, int strips) {
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
@@ -592,29 +598,29 @@ __global__ void __launch_bounds__(kPermThreads) dispatch_kernel(const PermuteArg
                     strips);
        at.more(); at.step()) {
     const int64_t t = at.row;
-    const int64_t v0 = static_cast<int64_t>(at.strip) * (32 * kDispU) + lane;
-    uint4 q[kDispU];
+    const int64_t v0 = static_cast<int64_t>(at.strip) * (32 * kU) + lane;
+    // many tokens: the cached index costs less than the lanes' exchange (48.5 us against 49.8)
+    const int row = kU == 1 && lane < a.k ? static_cast<int>(slot_row(a, t, lane)) : -1;
+    uint4 q[kU];
 #pragma unroll
-    for (int u = 0; u < kDispU; ++u)
+    for (int u = 0; u < kU; ++u)
       if (v0 + 32 * u < V) q[u] = __ldg(src + t * V + v0 + 32 * u);
     for (int j = 0; j < a.k; ++j) {
-      const int64_t r = slot_row(a, t, j);
+      const int64_t r = kU == 1 ? __shfl_sync(kFull, row, j) : slot_row(a, t, j);
       if (r < 0) continue;
 #pragma unroll
-      for (int u = 0; u < kDispU; ++u)
+      for (int u = 0; u < kU; ++u)
         if (v0 + 32 * u < V) dst[r * V + v0 + 32 * u] = q[u];
     }
   }
 }
 
-// A strip is 2 KB of each of the token's rows.  Longer pieces of a row at a
+// With many tokens a strip is 2 KB of each of the token's rows.  Longer pieces of a row at a
 // time are what HBM wants: 512-byte strips with more slots' loads in flight
 // took 66-73 us where these take 52 (8192 tokens, 8 slots, 2048 bf16).  The
 // token's rows and weights are held by lanes, so that no load of a vector
 // waits for one of an index.
-constexpr int kCombU = 4;
-
-template <bool kBf16, bool kWeighted>
+template <bool kBf16, bool kWeighted, int kU>
 __global__ void __launch_bounds__(kPermThreads, 4) combine_kernel(const PermuteArgs a, int64_t V, int strips) {
   constexpr int N = Vec<kBf16>::kN;
   pdl_wait_prior_grid();
@@ -627,17 +633,17 @@ __global__ void __launch_bounds__(kPermThreads, 4) combine_kernel(const PermuteA
                     strips);
        at.more(); at.step()) {
     const int64_t t = at.row;
-    const int64_t v0 = static_cast<int64_t>(at.strip) * (32 * kCombU) + lane;
+    const int64_t v0 = static_cast<int64_t>(at.strip) * (32 * kU) + lane;
     const int row = lane < a.k ? static_cast<int>(slot_row(a, t, lane)) : -1;
     const float weight = kWeighted && row >= 0 ? __ldg(a.weights + t * a.k + lane) : 0.0f;
-    float acc[kCombU][N] = {};
-#pragma unroll 2
+    float acc[kU][N] = {};
+#pragma unroll(kU == 1 ? 8 : 2)
     for (int j = 0; j < a.k; ++j) {
       const int r = __shfl_sync(kFull, row, j);
       const float w = __shfl_sync(kFull, weight, j);
       if (r < 0) continue;
 #pragma unroll
-      for (int u = 0; u < kCombU; ++u) {
+      for (int u = 0; u < kU; ++u) {
         if (v0 + 32 * u < V) {
           float f[N];
           unpack<kBf16>(__ldg(src + r * V + v0 + 32 * u), f);
@@ -647,7 +653,7 @@ __global__ void __launch_bounds__(kPermThreads, 4) combine_kernel(const PermuteA
       }
     }
 #pragma unroll
-    for (int u = 0; u < kCombU; ++u)
+    for (int u = 0; u < kU; ++u)
       if (v0 + 32 * u < V) dst[t * V + v0 + 32 * u] = pack<kBf16>(acc[u]);
   }
 }
@@ -722,20 +728,31 @@ static unsigned perm_grid(int64_t tasks, const void* fn) {
   return static_cast<unsigned>(need < most ? need : most);
 }
 
+template <int kU>
+static cudaError_t dispatch_u(const PermuteArgs& a, int64_t V, cudaStream_t s) {
+  const int strips = static_cast<int>((V + 32 * kU - 1) / (32 * kU));
+  auto kern = dispatch_kernel<kU>;
+  return launch_ex(kern, dim3(perm_grid(a.T * strips, reinterpret_cast<const void*>(kern))), dim3(kPermThreads), 0, s,
+                   true, a, V, strips);
+}
+
 cudaError_t launch_dispatch(const PermuteArgs& a, cudaStream_t s) {
   const int64_t V = a.H / (a.xt == AVR_BF16 ? 8 : 4);
-  const int strips = static_cast<int>((V + 32 * kDispU - 1) / (32 * kDispU));
-  return launch_ex(dispatch_kernel, dim3(perm_grid(a.T * strips, reinterpret_cast<const void*>(dispatch_kernel))),
-                   dim3(kPermThreads), 0, s, true, a, V, strips);
+  return a.T * V <= kFewVectors ? dispatch_u<1>(a, V, s) : dispatch_u<4>(a, V, s);
+}
+
+template <bool kBf16, bool kWeighted, int kU>
+static cudaError_t combine_u(const PermuteArgs& a, int64_t V, cudaStream_t s) {
+  const int strips = static_cast<int>((V + 32 * kU - 1) / (32 * kU));
+  auto kern = combine_kernel<kBf16, kWeighted, kU>;
+  return launch_ex(kern, dim3(perm_grid(a.T * strips, reinterpret_cast<const void*>(kern))), dim3(kPermThreads), 0, s,
+                   true, a, V, strips);
 }
 
 template <bool kBf16, bool kWeighted>
 static cudaError_t combine_t(const PermuteArgs& a, cudaStream_t s) {
   const int64_t V = a.H / Vec<kBf16>::kN;
-  const int strips = static_cast<int>((V + 32 * kCombU - 1) / (32 * kCombU));
-  auto kern = combine_kernel<kBf16, kWeighted>;
-  return launch_ex(kern, dim3(perm_grid(a.T * strips, reinterpret_cast<const void*>(kern))), dim3(kPermThreads), 0, s,
-                   true, a, V, strips);
+  return a.T * V <= kFewVectors ? combine_u<kBf16, kWeighted, 1>(a, V, s) : combine_u<kBf16, kWeighted, 4>(a, V, s);
 }
 
 cudaError_t launch_combine(const PermuteArgs& a, cudaStream_t s) {
