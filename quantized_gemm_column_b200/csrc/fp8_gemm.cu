@@ -32,7 +32,7 @@
 //
 // The tensor core's fp32 sums are cut off, not rounded, so a long sum of one
 // sign drifts (1e-6 relative over 4096 terms, 9e-6 over 16384).  An fp32
-// output is therefore summed in visits of at most 4096 of K: the first is
+// output is therefore summed in visits of at most 6144 of K: the first is
 // stored, the others are added to it by TMA reductions, which round to nearest,
 // in order.  A bf16 output's own rounding is 400 times that drift.
 //
