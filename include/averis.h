@@ -403,7 +403,10 @@ avr_status averis_moe_linear_dgrad(const void* D, avr_dtype dt, int64_t l_cap, c
  * (1 <= k <= 32), E experts (1 <= E <= 1024, k <= E for the router), H
  * features (H % 8 == 0).  ids, row, weights and their gradients are [T, k];
  * a negative id or row is a slot without an expert: it takes no row, adds
- * nothing and its gradient is 0, whatever its weight holds.  Buffers have
+ * nothing and its gradient is 0, whatever its weight holds.  No two slots
+ * share a row (moe_sort gives each its own); where a caller's do, a call that
+ * writes buffer rows leaves one slot's value in it.  Tensors start on 16
+ * bytes; ids, rows, counts, weights and dweights on 4.  Buffers have
  * l_cap rows (a multiple of 128); rows that hold no token are neither read
  * nor written.  An id >= E or a row >= l_cap latches AVR_ERR_INVALID_ARG and
  * counts as negative.  Sums in fp32, slots in ascending order: the same inputs give
@@ -464,7 +467,9 @@ avr_status moe_combine_bwd(const void* dY, const void* Yp, avr_dtype yt, int64_t
  * A power of two is what the tensor cores apply (block_scale, E8M0), so a
  * product needs no fp32 promotion between blocks.  A NaN or infinity latches
  * AVR_ERR_NONFINITE (the outputs are then undefined).
- * Sizes: m, n, K multiples of 16; l >= 0 tokens; all < 2^31.
+ * Sizes: m, n, K multiples of 16; l >= 0 tokens; all < 2^31.  Tensors, codes
+ * and scales start on 16 bytes, counts on 4.  Calls that share a workspace
+ * run on one stream, as everywhere in this library.
  * ------------------------------------------------------------------------- */
 
 /* codes  : rows * K bytes, row-major E4M3.
