@@ -230,6 +230,26 @@ def test_sort_is_exact(api, T, k, E, skew):
     assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(row.cpu().numpy(), rr)
 
 
+@pytest.mark.parametrize("T,k,E", [(256, 1, 256), (128, 2, 257), (257, 1, 9), (255, 1, 255), (7, 32, 33), (3, 5, 256)])
+def test_sort_around_one_small_block(api, T, k, E):
+    """Both sides of the sizes at which a smaller block does all: exact, an id
+    past the experts latched, a buffer too small refused."""
+    ids = _ids(T, k, E, 3 * T + k, skew=False)
+    ids[::5, 0] = -1
+    rc, rr, _, used = R.sort(ids, E)
+    counts, row, ws = _sort(api, ids, E, l_cap=used)
+    assert api.averis_check_status(ws) == 0
+    assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(row.cpu().numpy(), rr)
+    counts, row, ws = _sort(api, ids, E, l_cap=used - 128, ws=ws)
+    assert api.averis_check_status(ws) == api.AVR_ERR_INVALID_ARG
+    assert not counts.any() and (row == -1).all()
+    ids[T - 1, k - 1] = E
+    rc, rr, _, used = R.sort(ids, E)
+    counts, row, ws = _sort(api, ids, E, ws=ws)
+    assert api.averis_check_status(ws) == api.AVR_ERR_INVALID_ARG
+    assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(row.cpu().numpy(), rr)
+
+
 def test_sort_edges(api):
     # every slot dropped; every slot to one expert; no tokens
     for ids in (np.full((300, 4), -1, dtype=np.int32), np.full((300, 4), 8, dtype=np.int32),
@@ -340,6 +360,15 @@ def test_combine_and_its_gradients(api, T, k, E, H, dt):
     assert not got_w[row < 0].any()
     free = np.setdiff1d(np.arange(cap), row[row >= 0])
     assert (got_p[free] == 5.0).all()
+
+
+@pytest.mark.parametrize("T,k,E,H,dt", [(700, 5, 9, 520, "bf16"), (333, 4, 7, 1096, "f32"), (128, 2, 3, 2048, "bf16"),
+                                        (129, 2, 3, 2048, "bf16"), (40, 8, 9, 8200, "bf16"), (40, 3, 4, 4104, "f32")])
+def test_dispatch_and_combine_of_more_tokens(api, T, k, E, H, dt):
+    """The wide strips of many tokens, both sides of where they begin (32768
+    vectors of 16 bytes) and rows that end inside one."""
+    test_dispatch_and_its_gradient(api, T, k, E, H, dt)
+    test_combine_and_its_gradients(api, T, k, E, H, dt)
 
 
 def test_combine_gradients_against_differences(api):
