@@ -456,6 +456,17 @@ avr_status moe_combine_bwd(const void* dY, const void* Yp, avr_dtype yt, int64_t
                            const int32_t* row, const float* weights, int64_t l_cap, void* dYp, float* dweights,
                            void* ws, size_t ws_bytes, avr_stream stream);
 
+/* The same two with Yp in fp32 whatever the tokens' type yt (Y, dY, dYp): the
+ * experts' products are then rounded once, in Y, where a bf16 buffer rounds
+ * each of them before the sum as well.  That buffer is twice as large.
+ * Launches 1 kernel. */
+avr_status moe_combine_f32(const float* Yp, avr_dtype yt, int64_t T, int k, int64_t H, const int32_t* row,
+                           const float* weights, int64_t l_cap, void* Y, void* ws, size_t ws_bytes,
+                           avr_stream stream);
+avr_status moe_combine_f32_bwd(const void* dY, const float* Yp, avr_dtype yt, int64_t T, int k, int64_t H,
+                               const int32_t* row, const float* weights, int64_t l_cap, void* dYp, float* dweights,
+                               void* ws, size_t ws_bytes, avr_stream stream);
+
 /* -------------------------------------------------------------------------
  * 8-bit linear layer: E4M3 values with a scale for each block of 128
  *

@@ -130,6 +130,8 @@ _SIGS.update({
     "moe_dispatch_bwd": (_c_int, [_c_ptr] + _PERM + [_c_i64, _c_ptr] + _WS),
     "moe_combine": (_c_int, [_c_ptr] + _PERM + [_c_ptr, _c_i64, _c_ptr] + _WS),
     "moe_combine_bwd": (_c_int, [_c_ptr, _c_ptr] + _PERM + [_c_ptr, _c_i64, _c_ptr, _c_ptr] + _WS),
+    "moe_combine_f32": (_c_int, [_c_ptr] + _PERM + [_c_ptr, _c_i64, _c_ptr] + _WS),
+    "moe_combine_f32_bwd": (_c_int, [_c_ptr, _c_ptr] + _PERM + [_c_ptr, _c_i64, _c_ptr, _c_ptr] + _WS),
     "avr_fp8_scales_bytes": (_c_size, [_c_i64, _c_i64]),
     "fp8_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
     "fp8_quant": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_fp8] + _WS),
@@ -627,6 +629,33 @@ def moe_combine_bwd(dY, Yp, row, weights, dYp, dweights, ws, stream=None):
         _refuse_shape("moe_combine_bwd", (row, (T, k), _I32), (weights, (T, k), _F32), (dweights, (T, k), _F32),
                       (Yp, (l_cap, H), dY.dtype), (dYp, (l_cap, H), dY.dtype))
     _call("moe_combine_bwd", stream, ws, (dY, Yp, row, weights, dYp, dweights),
+          (dY.data_ptr(), Yp.data_ptr(), _dt(dY), T, k, H, row.data_ptr(), weights.data_ptr(), l_cap,
+           dYp.data_ptr(), dweights.data_ptr()))
+
+
+def moe_combine_f32(Yp, row, weights, Y, ws, stream=None):
+    """Yp is fp32, Y of either type."""
+    T, H = Y.shape
+    T_k = rT, k = row.shape
+    l_cap, pH = Yp.shape
+    if rT != T or pH != H or row.dtype is not _I32 or weights.shape != T_k or weights.dtype is not _F32 \
+            or Yp.dtype is not _F32:
+        _refuse_shape("moe_combine_f32", (row, (T, k), _I32), (weights, (T, k), _F32), (Yp, (l_cap, H), _F32))
+    _call("moe_combine_f32", stream, ws, (Yp, row, weights, Y),
+          (Yp.data_ptr(), _dt(Y), T, k, H, row.data_ptr(), weights.data_ptr(), l_cap, Y.data_ptr()))
+
+
+def moe_combine_f32_bwd(dY, Yp, row, weights, dYp, dweights, ws, stream=None):
+    """Yp is fp32, dY and dYp of one type, either."""
+    T, H = dY.shape
+    T_k = rT, k = row.shape
+    buf = l_cap, pH = Yp.shape
+    if rT != T or pH != H or row.dtype is not _I32 or weights.shape != T_k or weights.dtype is not _F32 \
+            or dweights.shape != T_k or dweights.dtype is not _F32 or Yp.dtype is not _F32 \
+            or dYp.shape != buf or dYp.dtype is not dY.dtype:
+        _refuse_shape("moe_combine_f32_bwd", (row, (T, k), _I32), (weights, (T, k), _F32), (dweights, (T, k), _F32),
+                      (Yp, (l_cap, H), _F32), (dYp, (l_cap, H), dY.dtype))
+    _call("moe_combine_f32_bwd", stream, ws, (dY, Yp, row, weights, dYp, dweights),
           (dY.data_ptr(), Yp.data_ptr(), _dt(dY), T, k, H, row.data_ptr(), weights.data_ptr(), l_cap,
            dYp.data_ptr(), dweights.data_ptr()))
 

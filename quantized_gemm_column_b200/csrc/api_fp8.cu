@@ -184,6 +184,34 @@ PermuteArgs permute_args(const void* src, void* dst, avr_dtype xt, int64_t T, in
   return a;
 }
 
+// f32_buffer: Yp is fp32 whatever the tokens' type yt
+avr_status combine(const void* Yp, bool f32_buffer, avr_dtype yt, int64_t T, int k, int64_t H, const int32_t* row,
+                   const float* weights, int64_t l_cap, void* Y, void* ws, size_t ws_bytes, avr_stream stream) {
+  if (T > 0 && !weights) return AVR_ERR_INVALID_ARG;
+  if (!aligned4(weights)) return AVR_ERR_MISALIGNED;
+  AVR_TRY(check_permute(Y, Yp, row, yt, T, k, H, l_cap, ws, ws_bytes));
+  if (T == 0) return AVR_OK;
+  PermuteArgs a = permute_args(Yp, Y, yt, T, k, H, row, l_cap, ws);
+  a.f32_buffer = f32_buffer;
+  a.weights = weights;
+  return cuda_status(launch_combine(a, stream));
+}
+
+avr_status combine_bwd(const void* dY, const void* Yp, bool f32_buffer, avr_dtype yt, int64_t T, int k, int64_t H,
+                       const int32_t* row, const float* weights, int64_t l_cap, void* dYp, float* dweights, void* ws,
+                       size_t ws_bytes, avr_stream stream) {
+  if (T > 0 && (!weights || !dweights || (l_cap > 0 && !dYp))) return AVR_ERR_INVALID_ARG;
+  if (!aligned4(weights) || !aligned4(dweights) || !aligned16(dYp)) return AVR_ERR_MISALIGNED;
+  AVR_TRY(check_permute(dY, Yp, row, yt, T, k, H, l_cap, ws, ws_bytes));
+  if (T == 0) return AVR_OK;
+  PermuteArgs a = permute_args(dY, dYp, yt, T, k, H, row, l_cap, ws);
+  a.yp = Yp;
+  a.f32_buffer = f32_buffer;
+  a.weights = weights;
+  a.dweights = dweights;
+  return cuda_status(launch_combine_bwd(a, stream));
+}
+
 }  // namespace
 }  // namespace avr
 
@@ -252,27 +280,25 @@ avr_status moe_dispatch_bwd(const void* dXp, avr_dtype xt, int64_t T, int k, int
 
 avr_status moe_combine(const void* Yp, avr_dtype yt, int64_t T, int k, int64_t H, const int32_t* row,
                        const float* weights, int64_t l_cap, void* Y, void* ws, size_t ws_bytes, avr_stream stream) {
-  if (T > 0 && !weights) return AVR_ERR_INVALID_ARG;
-  if (!aligned4(weights)) return AVR_ERR_MISALIGNED;
-  AVR_TRY(check_permute(Y, Yp, row, yt, T, k, H, l_cap, ws, ws_bytes));
-  if (T == 0) return AVR_OK;
-  PermuteArgs a = permute_args(Yp, Y, yt, T, k, H, row, l_cap, ws);
-  a.weights = weights;
-  return cuda_status(launch_combine(a, stream));
+  return combine(Yp, false, yt, T, k, H, row, weights, l_cap, Y, ws, ws_bytes, stream);
 }
 
 avr_status moe_combine_bwd(const void* dY, const void* Yp, avr_dtype yt, int64_t T, int k, int64_t H,
                            const int32_t* row, const float* weights, int64_t l_cap, void* dYp, float* dweights,
                            void* ws, size_t ws_bytes, avr_stream stream) {
-  if (T > 0 && (!weights || !dweights || (l_cap > 0 && !dYp))) return AVR_ERR_INVALID_ARG;
-  if (!aligned4(weights) || !aligned4(dweights) || !aligned16(dYp)) return AVR_ERR_MISALIGNED;
-  AVR_TRY(check_permute(dY, Yp, row, yt, T, k, H, l_cap, ws, ws_bytes));
-  if (T == 0) return AVR_OK;
-  PermuteArgs a = permute_args(dY, dYp, yt, T, k, H, row, l_cap, ws);
-  a.yp = Yp;
-  a.weights = weights;
-  a.dweights = dweights;
-  return cuda_status(launch_combine_bwd(a, stream));
+  return combine_bwd(dY, Yp, false, yt, T, k, H, row, weights, l_cap, dYp, dweights, ws, ws_bytes, stream);
+}
+
+avr_status moe_combine_f32(const float* Yp, avr_dtype yt, int64_t T, int k, int64_t H, const int32_t* row,
+                           const float* weights, int64_t l_cap, void* Y, void* ws, size_t ws_bytes,
+                           avr_stream stream) {
+  return combine(Yp, true, yt, T, k, H, row, weights, l_cap, Y, ws, ws_bytes, stream);
+}
+
+avr_status moe_combine_f32_bwd(const void* dY, const float* Yp, avr_dtype yt, int64_t T, int k, int64_t H,
+                               const int32_t* row, const float* weights, int64_t l_cap, void* dYp, float* dweights,
+                               void* ws, size_t ws_bytes, avr_stream stream) {
+  return combine_bwd(dY, Yp, true, yt, T, k, H, row, weights, l_cap, dYp, dweights, ws, ws_bytes, stream);
 }
 
 // ---------------------------------------------------------------------------

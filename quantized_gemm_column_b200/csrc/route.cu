@@ -67,6 +67,18 @@ __device__ __forceinline__ uint4 pack(const float (&f)[Vec<kBf16>::kN]) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// the values of one 16-byte vector (of kBf16) to vector i of a tensor of kBf16Out
+template <bool kBf16, bool kBf16Out>
+__device__ __forceinline__ void store_vec(void* dst, int64_t i, const float (&f)[Vec<kBf16>::kN]) {
+  if constexpr (kBf16 == kBf16Out) {
+    static_cast<uint4*>(dst)[i] = pack<kBf16>(f);
+  } else {
+    static_assert(!kBf16, "fp32 to bf16");
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    static_cast<uint2*>(dst)[i] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
 
 }  // namespace
 
@@ -634,8 +646,8 @@ __global__ void __launch_bounds__(kPermThreads) dispatch_kernel(const PermuteArg
 // time are what HBM wants: 512-byte strips with more slots' loads in flight
 // took 66-73 us where these take 52 (8192 tokens, 8 slots, 2048 bf16).  The
 // token's rows and weights are held by lanes, so that no load of a vector
-// waits for one of an index.
-template <bool kBf16, bool kWeighted, int kU>
+// waits for one of an index.  kBf16 is the buffer's type, kBf16Out the tokens'.
+template <bool kBf16, bool kBf16Out, bool kWeighted, int kU>
 __global__ void __launch_bounds__(kPermThreads, 4) combine_kernel(const PermuteArgs a, int64_t V, int strips) {
   constexpr int N = Vec<kBf16>::kN;
   pdl_wait_prior_grid();
@@ -643,7 +655,6 @@ __global__ void __launch_bounds__(kPermThreads, 4) combine_kernel(const PermuteA
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kPermThreads / 32);
   const uint4* src = static_cast<const uint4*>(a.src);
-  uint4* dst = static_cast<uint4*>(a.dst);
   for (StripWalk at(static_cast<int64_t>(blockIdx.x) * (kPermThreads / 32) + (threadIdx.x >> 5), warps, a.T * strips,
                     strips);
        at.more(); at.step()) {
@@ -669,7 +680,7 @@ __global__ void __launch_bounds__(kPermThreads, 4) combine_kernel(const PermuteA
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-      if (v0 + 32 * u < V) dst[t * V + v0 + 32 * u] = pack<kBf16>(acc[u]);
+      if (v0 + 32 * u < V) store_vec<kBf16, kBf16Out>(a.dst, t * V + v0 + 32 * u, acc[u]);
   }
 }
 
@@ -678,9 +689,10 @@ __global__ void __launch_bounds__(kPermThreads, 4) combine_kernel(const PermuteA
 // as many threads as make whole passes over the row's vectors, 128 at most.
 constexpr int kBwdThreads = 128, kBwdJ = 2;
 
-template <bool kBf16>
+// kBf16 is the type of dY and dYp, kBf16Buf that of Yp.
+template <bool kBf16, bool kBf16Buf>
 __global__ void __launch_bounds__(kBwdThreads) combine_bwd_kernel(const PermuteArgs a, int64_t V) {
-  constexpr int N = Vec<kBf16>::kN;
+  constexpr int N = Vec<kBf16>::kN, M = Vec<kBf16Buf>::kN, Q = N / M;      // Q vectors of Yp beside one of dY
   __shared__ float s_dot[kBwdThreads / 32][kMaxSlots];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
@@ -702,22 +714,28 @@ __global__ void __launch_bounds__(kBwdThreads) combine_bwd_kernel(const PermuteA
         dot[j] = 0.0f;
       }
       for (int64_t v = threadIdx.x; v < V; v += blockDim.x) {
-        uint4 q[kBwdJ];
+        uint4 q[kBwdJ][Q];
         float d[N];
 #pragma unroll
-        for (int j = 0; j < kBwdJ; ++j)
-          if (r[j] >= 0) q[j] = __ldg(yp + r[j] * V + v);
+        for (int j = 0; j < kBwdJ; ++j) {
+#pragma unroll
+          for (int u = 0; u < Q; ++u)
+            if (r[j] >= 0) q[j][u] = __ldg(yp + (r[j] * V + v) * Q + u);
+        }
         unpack<kBf16>(__ldg(dy + t * V + v), d);
 #pragma unroll
         for (int j = 0; j < kBwdJ; ++j) {
           if (r[j] < 0) continue;
-          float y[N], o[N];
-          unpack<kBf16>(q[j], y);
+          float o[N];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            dot[j] = fmaf(d[i], y[i], dot[j]);
-            o[i] = w[j] * d[i];
+          for (int u = 0; u < Q; ++u) {
+            float y[M];
+            unpack<kBf16Buf>(q[j][u], y);
+#pragma unroll
+            for (int i = 0; i < M; ++i) dot[j] = fmaf(d[u * M + i], y[i], dot[j]);
           }
+#pragma unroll
+          for (int i = 0; i < N; ++i) o[i] = w[j] * d[i];
           dst[r[j] * V + v] = pack<kBf16>(o);
         }
       }
@@ -756,28 +774,31 @@ cudaError_t launch_dispatch(const PermuteArgs& a, cudaStream_t s) {
   return a.T * V <= kFewVectors ? dispatch_u<1>(a, V, s) : dispatch_u<4>(a, V, s);
 }
 
-template <bool kBf16, bool kWeighted, int kU>
+template <bool kBf16, bool kBf16Out, bool kWeighted, int kU>
 static cudaError_t combine_u(const PermuteArgs& a, int64_t V, cudaStream_t s) {
   const int strips = static_cast<int>((V + 32 * kU - 1) / (32 * kU));
-  auto kern = combine_kernel<kBf16, kWeighted, kU>;
+  auto kern = combine_kernel<kBf16, kBf16Out, kWeighted, kU>;
   return launch_ex(kern, dim3(perm_grid(a.T * strips, reinterpret_cast<const void*>(kern))), dim3(kPermThreads), 0, s,
                    true, a, V, strips);
 }
 
-template <bool kBf16, bool kWeighted>
+template <bool kBf16, bool kBf16Out, bool kWeighted>
 static cudaError_t combine_t(const PermuteArgs& a, cudaStream_t s) {
   const int64_t V = a.H / Vec<kBf16>::kN;
-  return a.T * V <= kFewVectors ? combine_u<kBf16, kWeighted, 1>(a, V, s) : combine_u<kBf16, kWeighted, 4>(a, V, s);
+  return a.T * V <= kFewVectors ? combine_u<kBf16, kBf16Out, kWeighted, 1>(a, V, s)
+                                : combine_u<kBf16, kBf16Out, kWeighted, 4>(a, V, s);
 }
 
 cudaError_t launch_combine(const PermuteArgs& a, cudaStream_t s) {
-  if (a.weights != nullptr) return a.xt == AVR_BF16 ? combine_t<true, true>(a, s) : combine_t<false, true>(a, s);
-  return a.xt == AVR_BF16 ? combine_t<true, false>(a, s) : combine_t<false, false>(a, s);
+  const bool bf16 = a.xt == AVR_BF16;
+  if (a.weights == nullptr) return bf16 ? combine_t<true, true, false>(a, s) : combine_t<false, false, false>(a, s);
+  if (a.f32_buffer && bf16) return combine_t<false, true, true>(a, s);
+  return bf16 ? combine_t<true, true, true>(a, s) : combine_t<false, false, true>(a, s);
 }
 
-template <bool kBf16>
+template <bool kBf16, bool kBf16Buf>
 static cudaError_t combine_bwd_t(const PermuteArgs& a, cudaStream_t s) {
-  auto kern = combine_bwd_kernel<kBf16>;
+  auto kern = combine_bwd_kernel<kBf16, kBf16Buf>;
   const int64_t V = a.H / Vec<kBf16>::kN, passes = (V + kBwdThreads - 1) / kBwdThreads;
   const int threads = static_cast<int>(((V + passes - 1) / passes + 31) / 32 * 32);
   const int64_t most = static_cast<int64_t>(sm_count()) *
@@ -786,7 +807,8 @@ static cudaError_t combine_bwd_t(const PermuteArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_combine_bwd(const PermuteArgs& a, cudaStream_t s) {
-  return a.xt == AVR_BF16 ? combine_bwd_t<true>(a, s) : combine_bwd_t<false>(a, s);
+  if (a.xt != AVR_BF16) return combine_bwd_t<false, false>(a, s);
+  return a.f32_buffer ? combine_bwd_t<true, false>(a, s) : combine_bwd_t<true, true>(a, s);
 }
 
 }  // namespace avr

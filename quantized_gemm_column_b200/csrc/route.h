@@ -43,6 +43,7 @@ struct PermuteArgs {
   const float* weights;    // [T, k]; combine: null = all 1 (dispatch_bwd)
   float* dweights;         // combine_bwd
   avr_dtype xt;
+  bool f32_buffer;         // combine, combine_bwd: Yp is fp32 whatever xt
   int64_t T, H, l_cap;
   int k;
   uint32_t* status;

@@ -194,3 +194,19 @@ def test_plain_router_on_hand_cases():
     counts, row, off, used = R.sort(np.array([[1, 0], [1, -1], [0, 1]]), 3)
     assert counts.tolist() == [2, 3, 0] and off.tolist() == [0, 128, 256] and used == 256
     assert row.tolist() == [[128, 0], [129, -1], [1, 130]]
+
+
+def test_combine_f32_validation(api):
+    lib = api.load()
+    INV, SHAPE, MIS, SMALL = (api.AVR_ERR_INVALID_ARG, api.AVR_ERR_UNSUPPORTED_SHAPE, api.AVR_ERR_MISALIGNED,
+                              api.AVR_ERR_WORKSPACE_TOO_SMALL)
+    perm = dict(dt=1, T=4, k=2, H=64, row=P(16))
+    comb = _call(lib, "moe_combine_f32", dict(src=P(16), **perm, w=P(16), l_cap=128, dst=P(16), **WS))
+    combb = _call(lib, "moe_combine_f32_bwd", dict(dY=P(16), src=P(16), **perm, w=P(16), l_cap=128, dst=P(16), dw=P(16),
+                                                   **WS))
+    for f in (comb, combb):
+        assert f(dt=3) == INV and f(src=None) == INV and f(dst=None) == INV and f(row=None) == INV and f(w=None) == INV
+        assert f(H=60) == SHAPE and f(H=0) == SHAPE and f(k=40) == SHAPE and f(l_cap=130) == SHAPE and f(T=-1) == SHAPE
+        assert f(src=P(8)) == MIS and f(dst=P(8)) == MIS and f(row=P(18)) == MIS and f(w=P(18)) == MIS
+        assert f(ws_bytes=16639) == SMALL and f(ws=None) == INV and f(T=0, src=None, dst=None, row=None) == api.AVR_OK
+    assert combb(dw=None) == INV and combb(dw=P(18)) == MIS and combb(dY=None) == INV and combb(dY=P(8)) == MIS

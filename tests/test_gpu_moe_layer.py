@@ -219,3 +219,37 @@ def test_binding_refuses_what_a_kernel_cannot_take(api):
         assert e.value.status == api.AVR_ERR_INVALID_ARG
     with pytest.raises(TypeError):
         api.moe_dispatch(layer.X.half(), layer.row, layer.Xp.half(), layer.ws)
+
+
+def test_layer_of_bf16_tokens_rounds_its_outputs_once(api):
+    """From logits to output with the experts' products held in fp32: against
+    fp64, the products' and the sums' fp32 error and one rounding to bf16.  A
+    bf16 buffer's outputs leave that bound, since slots of both signs cancel."""
+    T, E, k, m, n = 200, 6, 3, 256, 384
+    layer = Layer(api, T, E, k, m, n, seed=11)
+    layer.forward()
+    rounded = layer.Y.clone()
+    xq = api.FP8Tensor(layer.cap, m)
+    Yp = torch.empty(layer.cap, n, device="cuda")
+    api.fp8_moe_dispatch(layer.X, layer.row, xq, layer.ws)
+    api.fp8_moe_gemm(xq, layer.counts, layer.w_fwd, Yp, layer.ws)
+    api.moe_combine_f32(Yp, layer.row, layer.w, layer.Y, layer.ws)
+    assert api.averis_check_status(layer.ws) == 0
+    ids, w = layer.ids.cpu().numpy(), layer.w.double().cpu().numpy()
+    x = R.deq(layer.X.double().cpu().numpy())
+    ref, err = np.zeros((T, n)), np.zeros((T, n))
+    for e in range(E):
+        We = R.deq(layer.W[e].double().cpu().numpy(), (128, 128))
+        share = (w * (ids == e)).sum(1)[:, None]
+        ref += share * (x @ We)
+        # m products in fp32, their sum a term of k
+        err += (m + k) * 2.0 ** -24 * share * (np.abs(x) @ np.abs(We))
+    tol = err * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
+    assert np.all(np.abs(layer.Y.double().cpu().numpy() - ref) <= tol)
+    assert np.any(np.abs(rounded.double().cpu().numpy() - ref) > tol)
+    # and the way back
+    dYp = torch.empty(layer.cap, n, dtype=torch.bfloat16, device="cuda")
+    api.moe_combine_f32_bwd(layer.dY, Yp, layer.row, layer.w, dYp, layer.dw, layer.ws)
+    assert api.averis_check_status(layer.ws) == 0
+    terms = layer.dY.double().cpu().numpy()[:, None] * Yp.double().cpu().numpy()[layer.row.cpu().numpy()]
+    assert np.all(np.abs(layer.dw.double().cpu().numpy() - terms.sum(-1)) <= n * 2.0 ** -24 * np.abs(terms).sum(-1))

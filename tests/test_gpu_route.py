@@ -419,3 +419,73 @@ def test_no_tokens(api):
     api.moe_combine(buf, row, z(0, 2), z(0, 64), ws)
     api.moe_combine_bwd(z(0, 64), buf, row, z(0, 2), buf, z(0, 2), ws)
     assert api.averis_check_status(ws) == 0 and (buf == 3.0).all()
+
+
+@pytest.mark.parametrize("T,k,E,H", SIZES + [(700, 5, 9, 520), (128, 2, 3, 1024), (129, 2, 3, 1024), (40, 8, 9, 4104)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_combine_of_an_fp32_buffer_and_its_gradients(api, T, k, E, H, dt):
+    """Yp in fp32, tokens of either type; both sides of where the wide strips
+    begin (32768 vectors of the buffer) and rows that end inside one."""
+    row, cap, t, w = _case(api, T, k, E, H, dt, seed=6)
+    ws = api.moe_route_workspace(T, k, E)
+    rc, wc = torch.from_numpy(row).cuda(), w.cuda()
+    Yp = torch.randn(cap, H, generator=torch.Generator().manual_seed(T))
+    _fill_free(Yp, row, float("nan"))
+    Y = torch.full((T, H), 5.0, dtype=DT[dt], device="cuda")
+    api.moe_combine_f32(Yp.cuda(), rc, wc, Y, ws)
+    dY = t(T, H)
+    dYp = torch.full((cap, H), 5.0, dtype=DT[dt], device="cuda")
+    dw = torch.full((T, k), 5.0, device="cuda")
+    api.moe_combine_f32_bwd(dY.cuda(), Yp.cuda(), rc, wc, dYp, dw, ws)
+    assert api.averis_check_status(ws) == 0
+    # as in test_combine_and_its_gradients
+    e, wn, d = EPS[DT[dt]], w.double().numpy(), dY.double().numpy()
+    ref, mag = np.zeros((T, H)), np.zeros((T, H))
+    got_p, got_w = dYp.double().cpu().numpy(), dw.double().cpu().numpy()
+    for i, j in zip(*np.nonzero(row >= 0)):
+        y = Yp[row[i, j]].double().numpy()
+        ref[i] += wn[i, j] * y
+        mag[i] += np.abs(wn[i, j] * y)
+        p = wn[i, j] * d[i]
+        assert np.all(np.abs(got_p[row[i, j]] - p) <= (e + 2.0 ** -24) * np.abs(p))
+        assert abs(got_w[i, j] - (d[i] * y).sum()) <= H * 2.0 ** -24 * np.abs(d[i] * y).sum()
+    # the sum in fp32, rounded once to the tokens' type; the sum's own error can move that by its size again
+    assert np.all(np.abs(Y.double().cpu().numpy() - ref) <= k * 2.0 ** -24 * mag * (1 + e) + e * np.abs(ref))
+    assert not got_w[row < 0].any()
+    free = np.setdiff1d(np.arange(cap), row[row >= 0])
+    assert (got_p[free] == 5.0).all()
+    if dt == "f32":                                               # the other entry point's bits
+        Z, dZp, dz = torch.empty_like(Y), dYp.clone(), torch.empty_like(dw)
+        api.moe_combine(Yp.cuda(), rc, wc, Z, ws)
+        api.moe_combine_bwd(dY.cuda(), Yp.cuda(), rc, wc, dZp, dz, ws)
+        assert torch.equal(Y, Z) and torch.equal(dYp, dZp) and torch.equal(dw, dz)
+
+
+def test_combine_of_an_fp32_buffer_edges(api):
+    """No tokens, rows past the buffer, and what the binding refuses."""
+    ws = api.moe_route_workspace(4, 2, 2)
+    z = lambda *s, d=torch.float32: torch.zeros(*s, dtype=d, device="cuda")      # noqa: E731
+    bf, i32 = torch.bfloat16, torch.int32
+    none, buf = z(0, 2, d=i32), torch.full((128, 64), 3.0, device="cuda")
+    dbuf = torch.full((128, 64), 4.0, dtype=bf, device="cuda")
+    api.moe_combine_f32(buf, none, z(0, 2), z(0, 64, d=bf), ws)
+    api.moe_combine_f32_bwd(z(0, 64, d=bf), buf, none, z(0, 2), dbuf, z(0, 2), ws)
+    assert api.averis_check_status(ws) == 0 and (buf == 3.0).all() and (dbuf == 4.0).all()
+    row = torch.tensor([[0, 128], [1, -1], [2 ** 31 - 1, 2], [3, 4]], dtype=i32, device="cuda")
+    w, Y, dw = torch.ones(4, 2, device="cuda"), z(4, 64, d=bf), z(4, 2)
+    for call in (lambda: api.moe_combine_f32(buf, row, w, Y, ws),
+                 lambda: api.moe_combine_f32_bwd(Y, buf, row, w, dbuf, dw, ws)):
+        call()
+        assert api.averis_check_status(ws) == api.AVR_ERR_INVALID_ARG
+    assert Y[:, 0].tolist() == [3.0, 3.0, 3.0, 6.0] and dw[:, 1].tolist() == [0.0, 0.0, 576.0, 1152.0]
+    assert torch.equal(dbuf[:5], Y[[0, 1, 2, 3, 3]]) and (dbuf[5:] == 4.0).all()
+    for call in (lambda: api.moe_combine_f32(buf.bfloat16(), row, w, Y, ws),
+                 lambda: api.moe_combine_f32(buf, row, w.bfloat16(), Y, ws),
+                 lambda: api.moe_combine_f32(buf, row, w, Y[:3], ws),
+                 lambda: api.moe_combine_f32(buf.t().contiguous().t(), row, w, Y, ws),
+                 lambda: api.moe_combine_f32_bwd(Y, buf, row, w, z(128, 64), dw, ws),
+                 lambda: api.moe_combine_f32_bwd(Y, buf.bfloat16(), row, w, dbuf, dw, ws),
+                 lambda: api.moe_combine_f32_bwd(Y, buf, row, w, dbuf, dw[:, :1].contiguous(), ws)):
+        with pytest.raises(api.AverisError) as e:
+            call()
+        assert e.value.status == api.AVR_ERR_INVALID_ARG
