@@ -408,8 +408,8 @@ def _own_run(st):
         a.moe_route(st["logits"], True, st["ids"], st["weights"], ws)
         a.moe_sort(st["ids"], st["Yp"].shape[0], st["counts"], st["row"], ws)
         a.fp8_moe_dispatch(st["X"], st["row"], h["xq"], ws)
-        a.fp8_moe_gemm(h["xq"], st["counts"], h["w_fwd"], st["Yp"], ws)
-        a.moe_combine(st["Yp"], st["row"], st["weights"], st["Y"], ws)
+        a.fp8_moe_gemm(h["xq"], st["counts"], h["w_fwd"], h["Yp"], ws)
+        a.moe_combine_f32(h["Yp"], st["row"], st["weights"], st["Y"], ws)
         return dict(ids=st["ids"], weights=st["weights"], counts=st["counts"], row=st["row"], Y=st["Y"])
     a.fp8_moe_quant_weights(st["W"], h["w_fwd"], h["w_dgrad"], ws)
     a.fp8_moe_linear_fwd(st["X"], st["counts"], h["w_fwd"], st["Y"], ws)
@@ -436,8 +436,9 @@ def _handle(a, st):
     E = c["E"]
     if not c["train"]:
         cap = st["Yp"].shape[0]
+        # the experts' products in fp32, so that the outputs are rounded once, as in the definition
         return dict(ws=a.fp8_moe_workspace(cap, m, n, E, c["T"] * c["k"]), xq=a.FP8Tensor(cap, m),
-                    w_fwd=a.FP8Tensor.of(st["w_codes"], st["w_scales"]))
+                    Yp=torch.empty(cap, n, device="cuda"), w_fwd=a.FP8Tensor.of(st["w_codes"], st["w_scales"]))
     return dict(ws=a.fp8_moe_workspace(st["X"].shape[0], m, n, E), w_fwd=a.FP8Tensor(E * n, m),
                 w_dgrad=a.FP8Tensor(E * m, n))
 
