@@ -426,8 +426,8 @@ avr_status moe_route(const void* logits, avr_dtype lt, int64_t T, int E, int k, 
 /* Gradient of the weights to the logits, dlogits [T, E] in lt, with s =
  * sum_j dw_j w_j: at the chosen experts w_j (dw_j - s), 0 elsewhere (norm =
  * 1; logits are not read and may be NULL), or p_e (dw_e - s) with the softmax
- * p over all E and dw_e = 0 for the experts not chosen (norm = 0).  Launches
- * 1 kernel. */
+ * p over all E and dw_e = 0 for the experts not chosen (norm = 0).  A token
+ * without experts has gradient 0 whatever its logits hold.  Launches 1 kernel. */
 avr_status moe_route_bwd(const void* logits, avr_dtype lt, int64_t T, int E, int k, int norm, const int32_t* ids,
                          const float* weights, const float* dweights, void* dlogits, void* ws, size_t ws_bytes,
                          avr_stream stream);

@@ -363,11 +363,13 @@ __global__ void __launch_bounds__(32 * route_warps(NV))
 #pragma unroll
   for (int i = 0; i < NV; ++i) d[i] = row[e0 + i];
   void* out = const_cast<void*>(row_of<kBf16>(dlogits, t * E));
-  if (norm) {
+  // a token without experts (a NaN or +inf logit leaves it so) has gradient 0,
+  // whatever its logits' exponentials are
+  if (norm || !__any_sync(kFull, id >= 0)) {
     store_lane<kBf16, NV>(out, e0, E, wide, d);
     return;
   }
-  const float c = den > 0.0f ? s / den : 0.0f;
+  const float c = den == 0.0f ? 0.0f : s / den;        // 0: every logit is -inf
 #pragma unroll
   for (int i = 0; i < NV; ++i) d[i] -= v[i] * c;
   store_lane<kBf16, NV>(out, e0, E, wide, d);

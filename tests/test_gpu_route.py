@@ -489,3 +489,32 @@ def test_combine_of_an_fp32_buffer_edges(api):
         with pytest.raises(api.AverisError) as e:
             call()
         assert e.value.status == api.AVR_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("E", [3, 40, 128, 300, 1024])
+def test_route_gradient_of_a_token_left_without_experts_is_zero(api, E, norm, dt, value):
+    """Tokens with NaN, +inf or nothing but -inf logits have no slot with an
+    expert: gradient 0, and the other tokens' is what it is without them."""
+    T, k = 9, 3
+    lt = _logits(T, E, dt, E)
+    clean = lt.clone()
+    lt[2, E - 1], lt[4, 0], lt[7] = value, value, value
+    lt[5] = -float("inf")
+    lt[8], lt[8, 1] = -float("inf"), value
+    gone = [2, 4, 5, 7, 8]
+    rest = [t for t in range(T) if t not in gone]
+    ids, w, ws = _route(api, lt, k, norm)
+    assert api.averis_check_status(ws) == api.AVR_ERR_NONFINITE
+    assert (ids[gone] == -1).all()
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(E)).cuda()
+    dl = torch.full((T, E), 9.0, dtype=DT[dt], device="cuda")
+    api.moe_route_bwd(lt.cuda(), norm, ids, w, dw, dl, ws)
+    assert api.averis_check_status(ws) == 0
+    assert (dl[gone] == 0).all()
+    cid, cw, _ = _route(api, clean, k, norm, ws)
+    cl = torch.empty_like(dl)
+    api.moe_route_bwd(clean.cuda(), norm, cid, cw, dw, cl, ws)
+    assert torch.equal(dl[rest], cl[rest])
