@@ -546,7 +546,8 @@ avr_status fp8_moe_quant_weights(const void* W, avr_dtype wt, int E, int64_t m, 
                                  const avr_fp8* w_dgrad, void* ws, size_t ws_bytes, avr_stream stream);
 
 /* moe_dispatch and the quantizer in one pass: row row[t, j] of xq [l_cap, K]
- * is Q(X[t]).  K % 128 == 0.  ws as the routing calls.  Launches 1 kernel. */
+ * is Q(X[t]); a token without a row may hold anything.  K % 128 == 0.  ws as
+ * the routing calls.  Launches 1 kernel. */
 avr_status fp8_moe_dispatch(const void* X, avr_dtype xt, int64_t T, int k, int64_t K, const int32_t* row,
                             const avr_fp8* xq, void* ws, size_t ws_bytes, avr_stream stream);
 

@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kQThreads, 4) fp8_quant_kernel(const Fp8QuantA
       if (kMode != Rows::kAll && r >= end) break;      // the whole warp
       uint4 codes;
       uint32_t word;
-      quant_strip<kBf16>(q[i], &codes, &word, &bad);
+      bool nonfinite = false;
+      quant_strip<kBf16>(q[i], &codes, &word, &nonfinite);
       auto put = [&](int64_t dst) {
         if (col < a.K) *reinterpret_cast<uint4*>(a.codes + dst * a.K + col) = codes;
         if (lane == 0) *reinterpret_cast<uint32_t*>(a.scales + scale_at(dst, 4 * strip, strips)) = word;
@@ -148,9 +149,15 @@ __global__ void __launch_bounds__(kQThreads, 4) fp8_quant_kernel(const Fp8QuantA
         for (int j = 0; j < a.k; ++j) {
           const int32_t dst = __ldg(a.row + r * a.k + j);
           if (dst >= a.l_cap) raise_status(a.status, AVR_ERR_INVALID_ARG);
-          if (dst >= 0 && dst < a.l_cap) put(dst);
+          if (dst >= 0 && dst < a.l_cap) {
+            put(dst);
+            bad |= nonfinite;             // a token without a row may hold anything
+          }
         }
-      } else if (r < end) {
+        continue;
+      }
+      bad |= nonfinite;
+      if (r < end) {
         put(r);
       } else if (lane == 0) {             // rows up to the next multiple of 128: zero scales
         *reinterpret_cast<uint32_t*>(a.scales + scale_at(r, 4 * strip, strips)) = 0u;

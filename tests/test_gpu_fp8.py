@@ -535,3 +535,33 @@ def test_offsets_past_32_bits(api):
     assert np.array_equal(got, q[: len(picks) - 1])
     api.fp8_quant_t(X, api.FP8Tensor(m, -(-l // 128) * 128), ws)
     assert api.averis_check_status(ws) == 0
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_dispatch_does_not_look_at_tokens_without_experts(api, dt, value):
+    """Padding and dropped tokens may hold anything, as in moe_dispatch; a
+    token with an expert may not."""
+    T, k, E, K = 70, 2, 3, 640
+    ids = inputs.rng_for(213, 1).integers(0, E, (T, k)).astype(np.int32)
+    ids[[3, 68, 69]] = -1
+    ids[10, 0] = -1
+    _, row, _, _ = R.sort(ids, E)
+    row = row.astype(np.int32)
+    cap = api.moe_max_rows(T, k, E)
+    X = _x(T, K, dt, 5)
+    X[3, 600], X[68], X[69, 0] = value, value, -value
+    xq, ws = api.FP8Tensor(cap, K), api.fp8_moe_workspace(cap, K, 128, E)
+    xq.codes.fill_(0x55), xq.scales.fill_(0x55)
+    api.fp8_moe_dispatch(X.cuda(), torch.from_numpy(row).cuda(), xq, ws)
+    assert api.averis_check_status(ws) == 0
+    live = [t for t in range(T) if t not in (3, 68, 69)]
+    q, s = R.quant(X[live].double().numpy())
+    wq, wsb = np.full((cap, K), R.e4m3_decode([0x55])[0]), np.full((cap, K // 128), 0x55, dtype=np.uint8)
+    for i, t in enumerate(live):
+        for j in np.nonzero(row[t] >= 0)[0]:
+            wq[row[t, j]], wsb[row[t, j]] = q[i], s[i]
+    _equal(xq, wq, wsb, rows=np.arange(cap))
+    X[10, K - 1] = value                                          # one slot with an expert, one without
+    api.fp8_moe_dispatch(X.cuda(), torch.from_numpy(row).cuda(), xq, ws)
+    assert api.averis_check_status(ws) == api.AVR_ERR_NONFINITE
