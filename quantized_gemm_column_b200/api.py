@@ -666,7 +666,7 @@ class FP8Tensor:
 
     def __init__(self, rows, K, device="cuda"):
         n = avr_fp8_scales_bytes(rows, K)
-        if rows > 0:
+        if rows > 0 and K != 0:          # [K, 0]: fp8_quant_t of no tokens
             _positive(n, "FP8Tensor")
         self._hold(torch.empty((int(rows), int(K)), dtype=torch.uint8, device=device),
                    torch.empty(n, dtype=torch.uint8, device=device))

@@ -210,3 +210,15 @@ def test_combine_f32_validation(api):
         assert f(src=P(8)) == MIS and f(dst=P(8)) == MIS and f(row=P(18)) == MIS and f(w=P(18)) == MIS
         assert f(ws_bytes=16639) == SMALL and f(ws=None) == INV and f(T=0, src=None, dst=None, row=None) == api.AVR_OK
     assert combb(dw=None) == INV and combb(dw=P(18)) == MIS and combb(dY=None) == INV and combb(dY=P(8)) == MIS
+
+
+def test_tensor_of_no_tokens(api):
+    """The output of fp8_quant_t for l = 0 is [K, 0]; a K the format does not
+    have is refused as before."""
+    t = api.FP8Tensor(64, 0, device="cpu")
+    assert t.codes.shape == (64, 0) and t.scales.numel() == 0 and (t.rows, t.K) == (64, 0)
+    assert api.FP8Tensor(0, 128, device="cpu").scales.numel() == 0
+    for K in (8, 100):
+        with pytest.raises(api.AverisError) as e:
+            api.FP8Tensor(64, K, device="cpu")
+        assert e.value.status == api.AVR_ERR_UNSUPPORTED_SHAPE

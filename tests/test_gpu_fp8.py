@@ -565,3 +565,11 @@ def test_dispatch_does_not_look_at_tokens_without_experts(api, dt, value):
     X[10, K - 1] = value                                          # one slot with an expert, one without
     api.fp8_moe_dispatch(X.cuda(), torch.from_numpy(row).cuda(), xq, ws)
     assert api.averis_check_status(ws) == api.AVR_ERR_NONFINITE
+
+
+def test_quantizers_of_no_tokens(api):
+    ws = api.fp8_workspace(0, 64, 32)
+    X = torch.zeros(0, 64, device="cuda")
+    api.fp8_quant(X, api.FP8Tensor(0, 64), ws)
+    api.fp8_quant_t(X, api.FP8Tensor(64, 0), ws)
+    assert api.averis_check_status(ws) == 0
