@@ -426,8 +426,8 @@ avr_status fp8_moe_dispatch(const void* X, avr_dtype xt, int64_t T, int k, int64
   if (!dtype_ok(xt) || !xq) return AVR_ERR_INVALID_ARG;
   if (!slots_ok(T, k) || !rows_ok(T) || !size16_ok(K) || K % 128 || !cap_ok(xq->rows)) return AVR_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return AVR_OK;
-  if (!X || !row) return AVR_ERR_INVALID_ARG;
-  AVR_TRY(check_fp8(xq, xq->rows, K));
+  if (!X || !row || xq->K != K) return AVR_ERR_INVALID_ARG;
+  if (xq->rows > 0) AVR_TRY(check_fp8(xq, xq->rows, K));
   if (!aligned16(X) || !aligned4(row)) return AVR_ERR_MISALIGNED;
   AVR_TRY(check_ws(ws, ws_bytes, kScratch));
   AVR_TRY(device_ok());

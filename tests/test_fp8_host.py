@@ -222,3 +222,16 @@ def test_tensor_of_no_tokens(api):
         with pytest.raises(api.AverisError) as e:
             api.FP8Tensor(64, K, device="cpu")
         assert e.value.status == api.AVR_ERR_UNSUPPORTED_SHAPE
+
+
+def test_fused_dispatch_takes_a_buffer_without_rows(api):
+    """Null codes and scales are refused with rows and taken without, as the
+    buffer of moe_dispatch; the call then gets as far as looking for a device."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is visible; this check is for a host without one")
+    lib = api.load()
+    disp = _call(lib, "fp8_moe_dispatch", dict(X=P(16), xt=1, T=4, k=2, K=256, row=P(16), xq=api.avr_fp8(16, 16, 128, 256),
+                                               **WS))
+    assert disp(xq=api.avr_fp8(None, None, 128, 256)) == api.AVR_ERR_INVALID_ARG
+    assert disp(xq=api.avr_fp8(None, None, 0, 128)) == api.AVR_ERR_INVALID_ARG
+    assert disp(xq=api.avr_fp8(None, None, 0, 256)) == api.AVR_ERR_NO_DEVICE

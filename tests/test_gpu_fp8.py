@@ -573,3 +573,20 @@ def test_quantizers_of_no_tokens(api):
     api.fp8_quant(X, api.FP8Tensor(0, 64), ws)
     api.fp8_quant_t(X, api.FP8Tensor(64, 0), ws)
     assert api.averis_check_status(ws) == 0
+
+
+def test_dispatch_into_a_buffer_without_rows(api):
+    """No expert of these tokens is held here: every row is negative, and the
+    fused dispatch takes an empty buffer as moe_dispatch does."""
+    T, k, K = 5, 2, 256
+    ws = api.fp8_moe_workspace(0, K, 128, 2)
+    X, row = torch.full((T, K), float("nan"), device="cuda"), torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    api.moe_dispatch(X, row, torch.empty(0, K, device="cuda"), ws)
+    api.fp8_moe_dispatch(X, row, api.FP8Tensor(0, K), ws)
+    assert api.averis_check_status(ws) == 0
+    row[1, 1] = 0
+    api.fp8_moe_dispatch(X, row, api.FP8Tensor(0, K), ws)
+    assert api.averis_check_status(ws) == api.AVR_ERR_INVALID_ARG
+    with pytest.raises(api.AverisError) as e:
+        api.fp8_moe_dispatch(X, row, api.FP8Tensor(0, 128), ws)
+    assert e.value.status == api.AVR_ERR_INVALID_ARG
