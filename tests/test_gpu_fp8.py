@@ -590,3 +590,151 @@ def test_dispatch_into_a_buffer_without_rows(api):
     with pytest.raises(api.AverisError) as e:
         api.fp8_moe_dispatch(X, row, api.FP8Tensor(0, 128), ws)
     assert e.value.status == api.AVR_ERR_INVALID_ARG
+
+
+def _pairs():
+    """CTA pairs that the products' grids hold at most."""
+    return torch.cuda.get_device_properties(0).multi_processor_count // 2
+
+
+def _row_tiles(counts):
+    """256-row tiles of the experts' buffer."""
+    return sum(-(-c // 256) for c in counts)
+
+
+@pytest.mark.parametrize("counts,m,n,dt,ot", [([1500, 0, 129, 700, 1, 1100], 256, 2048, "bf16", "bf16"),
+                                              ([1500, 0, 129, 700, 1, 1100], 256, 2048, "f32", "f32"),
+                                              ([0, 33, 0, 2000, 255, 257, 0, 1], 640, 1920, "bf16", "f32"),
+                                              ([1500, 0, 129, 700], 6400, 2048, "bf16", "f32"),
+                                              ([1500, 0, 129, 700], 6400, 2048, "bf16", "bf16")])
+def test_experts_many_rows_in_several_rounds(api, counts, m, n, dt, ot):
+    """The row tiles' product with more tiles than pairs: a pair goes from one
+    expert to another and from whole boxes of rows to cut ones."""
+    E = len(counts)
+    X, off = _buffer(counts, m, dt, 5)
+    cap = X.shape[0]
+    assert cap > 256 * E and _row_tiles(counts) * -(-n // 256) > _pairs()
+    ws = api.fp8_moe_workspace(cap, m, n, E)
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    W = torch.randn(E, m, n, generator=g, device="cuda").to(DT[dt])
+    f, d = api.FP8Tensor(E * n, m), api.FP8Tensor(E * m, n)
+    api.fp8_moe_quant_weights(W, f, d, ws)
+    D, _ = _buffer(counts, n, dt, 6)
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    Y, dX = (torch.full((cap, c), 7.0, dtype=DT[ot], device="cuda") for c in (n, m))
+    api.fp8_moe_linear_fwd(X.cuda(), cnt, f, Y, ws)
+    api.fp8_moe_linear_dgrad(D.cuda(), cnt, d, dX, ws)
+    assert api.averis_check_status(ws) == 0
+    wf, wd = (torch.from_numpy(R.tensor_value(t)).cuda().view(E, -1, t.K) for t in (f, d))
+    used = torch.zeros(cap, dtype=torch.bool, device="cuda")
+    for e, (o, c) in enumerate(zip(off, counts)):
+        used[o:o + c] = True
+        for got, x, w, K in ((Y, X, wf[e], m), (dX, D, wd[e], n)):
+            a = torch.from_numpy(R.deq(x[o:o + c].double().numpy())).cuda()
+            ref, mag = a @ w.t(), a.abs() @ w.abs().t()
+            # as in _check_product
+            assert ((got[o:o + c].double() - ref).abs() <= K * 2.0 ** -24 * mag + EPS[DT[ot]] * ref.abs()).all()
+    assert (Y[~used] == 7.0).all() and (dX[~used] == 7.0).all()
+
+
+CUT = [(2570, 2304, 3200), (1024, 6144, 6160), (1536, 1536, 3200)]
+
+
+def _cut_product(api, M, N, K):
+    a, b, ws = api.FP8Tensor(M, K), api.FP8Tensor(N, K), api.fp8_workspace(max(M, N), K, 16)
+    rng = torch.Generator(device="cuda").manual_seed(M + N)
+    for t in (a, b):
+        api.fp8_quant(torch.randn(t.rows, K, generator=rng, device="cuda") + 0.5, t, ws)
+    return a, b, ws
+
+
+@pytest.mark.parametrize("M,N,K", CUT)
+def test_gemm_cut_in_the_last_round(api, M, N, K):
+    """Two or three parts a tile, after a whole round of tiles (the first two)
+    or alone: right, the same bits again, and the workspace as it was."""
+    last = -(-M // 256) * -(-N // 256) % _pairs()
+    assert last and min(_pairs() // last, -(-K // 128) // 12) >= 2
+    a, b, ws = _cut_product(api, M, N, K)
+    Y, Z = torch.full((M, N), 7.0, device="cuda"), torch.full((M, N), 9.0, device="cuda")
+    ws[256:256 + 16384].zero_()
+    api.fp8_gemm(a, b, Y, ws)
+    api.fp8_gemm(a, b, Z, ws)
+    assert api.averis_check_status(ws) == 0 and not ws[:256 + 16384].any()
+    assert torch.equal(Y, Z)
+    A, B = (torch.from_numpy(R.tensor_value(t)).cuda() for t in (a, b))
+    ref, mag = A @ B.t(), A.abs() @ B.abs().t()
+    assert ((Y.double() - ref).abs() <= K * 2.0 ** -24 * mag + 2.0 ** -24 * ref.abs()).all()
+
+
+def test_two_cut_products_on_two_streams(api):
+    """Each with a workspace of its own: the bits of each alone."""
+    sets = [_cut_product(api, *s) for s in CUT[:2]]
+    new = lambda: [torch.full((a.rows, b.rows), 7.0, device="cuda") for a, b, _ in sets]     # noqa: E731
+    want, got = new(), new()
+    for (a, b, ws), Y in zip(sets, want):
+        api.fp8_gemm(a, b, Y, ws)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        for (a, b, ws), Y, s in zip(sets, got, streams):
+            api.fp8_gemm(a, b, Y, ws, s)
+    torch.cuda.synchronize()
+    for (a, b, ws), x, y in zip(sets, want, got):
+        assert api.averis_check_status(ws) == 0 and not ws[:256 + 16384].any()
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gradients_are_the_forward_differences(api, dt):
+    """Integers up to 15 are E4M3 values under any scale their blocks can have,
+    and the sums stay below 2^24, so quantizers and products are exact: L =
+    sum(D * Y) of the forward itself, at W +- V and X +- U, has differences
+    equal to <V, dW> and <U, dX> to the last bit; and the experts' likewise."""
+    g = torch.Generator().manual_seed(3)
+    ints = lambda hi, *s: torch.randint(-hi, hi + 1, s, generator=g).to(DT[dt])        # noqa: E731
+    l, m, n = 300, 144, 80
+    ws = api.fp8_workspace(l, m, n)
+    X, U, D, W, V = ints(7, l, m), ints(8, l, m), ints(15, l, n), ints(7, m, n), ints(8, m, n)
+    dW, dX, Y = torch.empty(m, n, device="cuda"), torch.empty(l, m, device="cuda"), torch.empty(l, n, device="cuda")
+    f, d = api.FP8Tensor(n, m), api.FP8Tensor(m, n)
+
+    def loss(x, w):
+        api.fp8_quant_weight(w.cuda(), f, d, ws)
+        api.fp8_linear_fwd(x.cuda(), f, Y, ws)
+        return (Y.double().cpu() * D.double()).sum().item()
+
+    by_w = (loss(X, W + V) - loss(X, W - V)) / 2
+    by_x = (loss(X + U, W) - loss(X - U, W)) / 2
+    loss(X, W)
+    api.fp8_linear_wgrad(X.cuda(), D.cuda(), dW, ws)
+    api.fp8_linear_dgrad(D.cuda(), d, dX, ws)
+    assert api.averis_check_status(ws) == 0
+    assert by_w == (dW.double().cpu() * V.double()).sum().item() and by_w != 0
+    assert by_x == (dX.double().cpu() * U.double()).sum().item() and by_x != 0
+
+    counts, m, n = [200, 0, 129, 1], 128, 256
+    E = len(counts)
+    off, cap = _segments(counts)
+    real = torch.zeros(cap, 1, dtype=torch.bool)
+    for o, c in zip(off, counts):
+        real[o:o + c] = True
+    wild = lambda t: torch.where(real, t, torch.full((), float("nan"), dtype=t.dtype))  # noqa: E731
+    X, U, D = wild(ints(7, cap, m)), ints(8, cap, m) * real, wild(ints(15, cap, n))
+    W, V = ints(7, E, m, n), ints(8, E, m, n)
+    ws, cnt = api.fp8_moe_workspace(cap, m, n, E), torch.tensor(counts, dtype=torch.int32, device="cuda")
+    dW, dX, Y = torch.empty(E, m, n, device="cuda"), torch.zeros(cap, m, device="cuda"), torch.zeros(cap, n, device="cuda")
+    f, d = api.FP8Tensor(E * n, m), api.FP8Tensor(E * m, n)
+
+    def moe_loss(x, w):
+        api.fp8_moe_quant_weights(w.cuda(), f, d, ws)
+        api.fp8_moe_linear_fwd(x.cuda(), cnt, f, Y, ws)
+        return (Y.double().cpu() * torch.where(real, D.double(), torch.zeros((), dtype=torch.float64))).sum().item()
+
+    by_w = (moe_loss(X, W + V) - moe_loss(X, W - V)) / 2
+    by_x = (moe_loss(X + U, W) - moe_loss(X - U, W)) / 2
+    moe_loss(X, W)
+    api.fp8_moe_linear_wgrad(X.cuda(), D.cuda(), cnt, dW, ws)
+    api.fp8_moe_linear_dgrad(D.cuda(), cnt, d, dX, ws)
+    assert api.averis_check_status(ws) == 0
+    assert by_w == (dW.double().cpu() * V.double()).sum().item() and by_w != 0
+    assert by_x == (dX.double().cpu() * U.double()).sum().item() and by_x != 0
