@@ -69,7 +69,6 @@ struct Cfg {
   static constexpr int kFirstEpiWarp = 8, kEpiWarps = 8;
   static constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
   static constexpr int kBoxBytes = 32 * 128;                    // an epilogue warp's staging box
-  static constexpr int kMaxVisit = 48;                          // blocks of K in one fp32 visit
   static constexpr int kOutOffset = kStages * (kABytes + kBBytes);
   static constexpr int kSfaOffset = kOutOffset + kEpiWarps * kBoxBytes;
   static constexpr int kSfbOffset = kSfaOffset + kSlots * kSfaBytes;
@@ -172,7 +171,7 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const Buffer* b, int i,
 // blocks of K in a visit of a tile of n: n, or the fewest equal visits for fp32
 template <bool kBf16Out>
 __device__ __forceinline__ int visit_length(int n) {
-  const int visits = (n + Cfg::kMaxVisit - 1) / Cfg::kMaxVisit;
+  const int visits = (n + kFp8MaxVisit - 1) / kFp8MaxVisit;
   return kBf16Out || visits < 2 ? n : (n + visits - 1) / visits;
 }
 

@@ -121,7 +121,7 @@ struct Fp8GemmArgs {
   const Fp8Table* table = nullptr;
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t s);
-constexpr int kFp8MaxVisit = 48;     // blocks of K that one fp32 accumulation spans
+constexpr int kFp8MaxVisit = 48;     // blocks of K that one accumulation of an fp32 output spans
 // the experts' products with few rows an expert (fp8_stream.cu): kRows
 constexpr int64_t kStreamBlocks = 2;
 bool fp8_stream_applies(const Fp8GemmArgs& a);
