@@ -113,12 +113,13 @@ avr_status averis_workspace_init(void* ws, size_t ws_bytes, avr_stream stream);
  * workspace status word since the last check (AVR_OK if none) and clear it.
  * After an error the whole 256-byte status block is cleared (the status
  * word, the one-kernel split's grid-barrier words, which a kernel that gave
- * up may have left part-counted, and the wait limit below), so the workspace
- * is ready for the next call. */
+ * up may have left part-counted, and the wait limit below), and so are the
+ * tickets and flags behind it: the workspace is ready for the next call. */
 avr_status averis_check_status(void* ws, avr_stream stream);
 
 /* Bound, in nanoseconds, of the waits in which a CTA waits for other CTAs
- * (the grid-wide barriers of averis_split_quant_fused); 0 restores the
+ * (the grid-wide barriers of averis_split_quant_fused, and the parts of an
+ * fp32 product of the 8-bit layer that is cut along K); 0 restores the
  * default of 2 s.  Written in stream order into the workspace's status block
  * (a zero-filled workspace has the default); averis_check_status resets it
  * to the default after an error.  A wait that runs out records

@@ -190,7 +190,8 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* s
                : "memory");
 }
 
-// a flag that a thread sets after its stores completed, and one of another CTA waits for and hands back
+// a flag that a thread sets after its stores completed, and one of another CTA
+// waits for, as long as the workspace's bound says, and hands back
 __device__ __forceinline__ void flag_set(uint32_t* f) {
   fence_proxy_async_global();
   __threadfence();
@@ -198,11 +199,16 @@ __device__ __forceinline__ void flag_set(uint32_t* f) {
 }
 __device__ __forceinline__ bool flag_take(uint32_t* f, uint32_t* status) {
   const uint64_t t0 = globaltimer_ns();
+  uint64_t limit = 0;
   for (;;) {
     uint32_t x;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(f) : "memory");
     if (x != 0u) break;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+    if (limit == 0) {                 // the status word is the workspace's first
+      limit = __ldcg(reinterpret_cast<const uint64_t*>(reinterpret_cast<const char*>(status) + kWaitLimitOffset));
+      if (limit == 0) limit = kWaitLimitNs;
+    }
+    if (globaltimer_ns() - t0 > limit) {
       raise_status(status, AVR_ERR_DEVICE_TIMEOUT);
       return false;
     }

@@ -738,3 +738,22 @@ def test_gradients_are_the_forward_differences(api, dt):
     assert api.averis_check_status(ws) == 0
     assert by_w == (dW.double().cpu() * V.double()).sum().item() and by_w != 0
     assert by_x == (dX.double().cpu() * U.double()).sum().item() and by_x != 0
+
+
+def test_wait_limit_of_a_cut_product(api):
+    """averis_set_wait_limit bounds every wait of a CTA for others, the parts
+    of a cut product among them: with 1 ns some part gives up at its first
+    poll, which is reported, and the workspace then gives the right bits."""
+    M, N, K = CUT[2]
+    a, b, ws = _cut_product(api, M, N, K)
+    want, got = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    api.fp8_gemm(a, b, want, ws)
+    assert api.averis_check_status(ws) == 0
+    api.averis_set_wait_limit(ws, 1)
+    api.fp8_gemm(a, b, got, ws)
+    assert api.averis_check_status(ws) == api.AVR_ERR_DEVICE_TIMEOUT
+    for limit in (0, 10_000_000_000):
+        api.averis_set_wait_limit(ws, limit)
+        got.fill_(7)
+        api.fp8_gemm(a, b, got, ws)
+        assert api.averis_check_status(ws) == 0 and torch.equal(got, want)
