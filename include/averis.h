@@ -67,12 +67,12 @@ typedef struct CUstream_st* avr_stream; /* same type as cudaStream_t */
 typedef enum {
   AVR_OK = 0,
   AVR_ERR_INVALID_ARG = 1,         /* null pointer, unknown enum value */
-  AVR_ERR_UNSUPPORTED_SHAPE = 2,   /* K % 64, N % 64, sizes out of range */
-  AVR_ERR_MISALIGNED = 3,          /* a pointer not 16-byte aligned */
+  AVR_ERR_UNSUPPORTED_SHAPE = 2,   /* a size out of the call's range, or not one of its multiples */
+  AVR_ERR_MISALIGNED = 3,          /* a pointer off its alignment */
   AVR_ERR_WORKSPACE_TOO_SMALL = 4,
   AVR_ERR_CUDA = 5,                /* a CUDA runtime/driver call failed */
   AVR_ERR_DEVICE_TIMEOUT = 6,      /* a device-side bounded wait expired */
-  AVR_ERR_NONFINITE = 7,           /* the input held NaN/Inf (mean or amax not finite) */
+  AVR_ERR_NONFINITE = 7,           /* the input held NaN/Inf (a mean, a largest magnitude or a logit) */
   AVR_ERR_NO_DEVICE = 8            /* current device is not an sm_100 GPU */
 } avr_status;
 

@@ -338,12 +338,12 @@ const char* averis_status_string(avr_status s) {
   switch (s) {
     case AVR_OK: return "ok";
     case AVR_ERR_INVALID_ARG: return "invalid argument";
-    case AVR_ERR_UNSUPPORTED_SHAPE: return "unsupported shape (need K % 64 == 0, N % 64 == 0, sizes < 2^31)";
-    case AVR_ERR_MISALIGNED: return "misaligned pointer (need 16-byte alignment, 256 for the workspace)";
+    case AVR_ERR_UNSUPPORTED_SHAPE: return "unsupported shape (a size out of the call's range, or not one of its multiples)";
+    case AVR_ERR_MISALIGNED: return "misaligned pointer (tensors on 16 bytes, indices and counts on 4 bytes, the workspace on 256)";
     case AVR_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
     case AVR_ERR_CUDA: return "CUDA error";
     case AVR_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
-    case AVR_ERR_NONFINITE: return "non-finite input (mean or amax is NaN/Inf)";
+    case AVR_ERR_NONFINITE: return "non-finite input (a mean, a largest magnitude or a logit is NaN/Inf)";
     case AVR_ERR_NO_DEVICE: return "no sm_100 device is current";
   }
   return "unknown status";

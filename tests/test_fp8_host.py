@@ -235,3 +235,13 @@ def test_fused_dispatch_takes_a_buffer_without_rows(api):
     assert disp(xq=api.avr_fp8(None, None, 128, 256)) == api.AVR_ERR_INVALID_ARG
     assert disp(xq=api.avr_fp8(None, None, 0, 128)) == api.AVR_ERR_INVALID_ARG
     assert disp(xq=api.avr_fp8(None, None, 0, 256)) == api.AVR_ERR_NO_DEVICE
+
+
+def test_status_texts_hold_for_every_call(api):
+    """The calls have different multiples and alignments, so the texts name
+    none that some call does not ask for."""
+    shape, mis = api.status_string(api.AVR_ERR_UNSUPPORTED_SHAPE), api.status_string(api.AVR_ERR_MISALIGNED)
+    assert shape.startswith("unsupported shape") and "64" not in shape
+    assert mis.startswith("misaligned pointer") and "4 bytes" in mis and "256" in mis
+    assert "logit" in api.status_string(api.AVR_ERR_NONFINITE)
+    assert api.status_string(99) == "unknown status"
