@@ -406,7 +406,7 @@ avr_status averis_moe_linear_dgrad(const void* D, avr_dtype dt, int64_t l_cap, c
  * a negative id or row is a slot without an expert: it takes no row, adds
  * nothing and its gradient is 0, whatever its weight holds.  No two slots
  * share a row (moe_sort gives each its own); where a caller's do, a call that
- * writes buffer rows leaves one slot's value in it.  Tensors start on 16
+ * writes buffer rows leaves pieces of one or the other in it.  Tensors start on 16
  * bytes; ids, rows, counts, weights and dweights on 4.  Buffers have
  * l_cap rows (a multiple of 128); rows that hold no token are neither read
  * nor written.  An id >= E or a row >= l_cap latches AVR_ERR_INVALID_ARG and
@@ -518,8 +518,15 @@ avr_status fp8_quant_t(const void* X, avr_dtype xt, int64_t l, int64_t K, const 
 avr_status fp8_quant_weight(const void* W, avr_dtype wt, int64_t m, int64_t n, const avr_fp8* w_fwd,
                             const avr_fp8* w_dgrad, void* ws, size_t ws_bytes, avr_stream stream);
 
-/* Y [M, N] = A B^T of A = a [M, K] and B = b [N, K], fp32 accumulation, in yt
- * (fp32 or bf16).  Launches 1 kernel. */
+/* Y [M, N] = A B^T of A = a [M, K] and B = b [N, K] in yt (fp32 or bf16).
+ * Launches 1 kernel.
+ * Accuracy of the products here and below: the tensor cores cut fp32 sums off
+ * instead of rounding them, by up to about 2^-23 of the running sum for every
+ * 32 of K (9e-6 of a sum of 16384 terms of one sign).  An fp32 output is summed
+ * over at most 6144 of K that way, and these sums are added with rounding; a
+ * bf16 output is one sum, off by up to about K 2^-28 of its terms' magnitudes:
+ * beyond K = 2^20 that can pass its own rounding, and such a sum belongs in an
+ * fp32 output. */
 avr_status fp8_gemm(const avr_fp8* a, const avr_fp8* b, void* Y, avr_dtype yt, void* ws, size_t ws_bytes,
                     avr_stream stream);
 
@@ -553,7 +560,13 @@ avr_status fp8_moe_dispatch(const void* X, avr_dtype xt, int64_t T, int k, int64
                             const avr_fp8* xq, void* ws, size_t ws_bytes, avr_stream stream);
 
 /* Y[r] = xq[r] W_e^T for the rows r of every expert e, w = the experts' [N, K]
- * stacked (rows = E N).  Launches 1 kernel. */
+ * stacked (rows = E N).  Launches 1 kernel.
+ * The rows of the buffer, not the counts, which only the device knows, choose
+ * between two kernels here and in fp8_moe_linear_fwd and _dgrad: up to 256 E
+ * rows (fp32 outputs: and K <= 6144) the one that reads the weights once for
+ * few rows an expert.  So a decoding step wants an l_cap of its own size
+ * (T k + 127 min(E, T k), rounded down to 128) and not the largest batch's;
+ * across that border the sums have another order. */
 avr_status fp8_moe_gemm(const avr_fp8* xq, const int32_t* counts, int E, const avr_fp8* w, void* Y, avr_dtype yt,
                         void* ws, size_t ws_bytes, avr_stream stream);
 

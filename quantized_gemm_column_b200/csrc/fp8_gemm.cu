@@ -34,7 +34,8 @@
 // sign drifts (1e-6 relative over 4096 terms, 9e-6 over 16384).  An fp32
 // output is therefore summed in visits of at most 6144 of K: the first is
 // stored, the others are added to it by TMA reductions, which round to nearest,
-// in order.  A bf16 output's own rounding is 400 times that drift.
+// in order.  A bf16 output is one sum: its own rounding is 400 times the drift
+// of 16384 terms; 2^20 terms of one sign can be cut off by as much.
 //
 // When the last round of an fp32 output has tiles for less than half of the
 // pairs, each of them is cut along K among several pairs (parts).  A part adds

@@ -168,11 +168,16 @@ bool fp8_skinny_applies(int64_t l, int64_t K, int64_t N) {
   const int64_t L = skinny_tokens(l);
   if (L * ((K + 511) / 512) * 512 > 48 * 1024) return false;      // the tokens in shared memory
   // This kernel's time goes as L N K, the quantizer's and the product's as K
-  // (one tile of rows whatever l).  us on the device, l = 1, 2, 4, 8 / theirs:
-  //   1024 -> 6144   4.1   5.1   7.3  12  /  8.7
-  //   4096 -> 4096   8.5  11.8  13.3  22  / 16.4
-  //   6144 -> 1024   5.7   6.9   9.1  15  / 21
-  //   1024 -> 1024   1.9   2.2   2.5   3.9 /  8.0
+  // (one tile of rows whatever l).  us on the device, l = 1, 2, 4, 8 / theirs
+  // (| where the rule changes over):
+  //   1024 -> 6144   4.1   5.1   7.3 | 12   /  8.6
+  //   4096 -> 4096   8.5  11.8  13.1 | 22   / 16.3
+  //    512 -> 8192   4.2   5.0   6.4 |  9.9 /  7.4
+  //   1024 -> 3584   3.7   4.4   4.7   7.7 |/  8.3
+  //   2048 -> 2048   3.9   4.9   5.5   9.2 |/ 10.9
+  //   8192 -> 1024   6.8   8.5  11.4  26.1 |/ 26.1
+  //   6144 -> 1024   5.7   6.9   9.1  15.3 |/ 21
+  //   1024 -> 1024   1.9   2.1   2.5   3.9 |/  7.9
   return L * N < (20000000 + 12000 * K) / K;
 }
 

@@ -184,7 +184,9 @@ __device__ __forceinline__ float key_value(uint32_t u) {
 
 // Each of the k steps takes the largest key of the warp and, among the lanes
 // that hold it, the lowest expert.  What bounds this is the number of
-// instructions (the logits are 17 MB for 32768 tokens of 128 experts), so a
+// instructions, 423 a token of 128 experts with 8 slots, of which 39 % go to
+// the pipe of half rate (the schedulers issue in 82 % of their cycles, that
+// pipe is busy in 64 %, and the logits are 17 MB for 32768 tokens), so a
 // step is kept short: a lane sorts its keys once (descending, the lower expert
 // first among equal ones; for up to 8, beyond that it searches), its best is
 // always the first, and the lowest lane that holds the step's maximum notes its
@@ -193,7 +195,9 @@ __device__ __forceinline__ float key_value(uint32_t u) {
 // reduction: 32768 tokens of 128 experts, 8 slots, take 14.9 us (13.9 with
 // `norm`), with experts 32 apart and a vote on ties 16.7 (15.7); 256 experts
 // 27.0 against 29.6.  The gradient of the 128 experts' tokens takes 9.5 us (5.4
-// with `norm`, which reads no logits).
+// with `norm`, which reads no logits).  From 257 experts on, a step searches the
+// lane's 16 or 32 keys: 32768 tokens of 512 experts take 45 us with 8 slots and
+// 134 with 32, of 1024 experts 80 and 239 (their logits are read in 10 and 20).
 template <bool kBf16, int NV>
 __global__ void __launch_bounds__(32 * route_warps(NV))
     route_kernel(const void* logits, int64_t T, int E, int k, int norm, bool wide, int32_t* ids, float* weights,
@@ -427,8 +431,10 @@ cudaError_t launch_route_bwd(const void* logits, avr_dtype lt, int64_t T, int E,
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 // A decoding step's slots take one round of one smaller block, whose barriers
-// and cleared counts are cheaper: 256 slots of 64 experts 2.4 us, with 1024
-// threads 3.1.  A thread is an expert in the scan, so E is bounded too.
+// and cleared counts are cheaper.  us with 256 threads / with 1024, 64 experts:
+// 64 slots 2.1 / 2.9, 256 slots 2.3 / 3.0, 384 slots 2.9 / 3.0, 512 slots 3.3 /
+// 3.3, 1024 slots 4.7 / 3.8.  A thread is an expert in the scan, so E is bounded
+// too.
 constexpr int kFewSlots = 256;
 static_assert(kSortThreads >= kMaxExperts, "one thread an expert");
 
@@ -610,9 +616,14 @@ __device__ __forceinline__ int64_t slot_row(const PermuteArgs& a, int64_t t, int
 
 // With few tokens (T times the 16-byte vectors of a row up to this) a strip is
 // one vector a lane, so that the work spreads over four times the warps and
-// all of a token's loads are in flight together: 64 tokens of 2048 bf16, 8
-// slots, dispatch 1.8 us against 2.3 and combine 3.2 against 3.5; 512 tokens
-// 3.8 and 5.4 against 3.7 and 4.2.
+// all of a token's loads are in flight together.  us with one vector a lane /
+// with four, 2048 bf16, 8 slots (thousands of vectors):
+//   tokens (vectors)   64 (16)      128 (33)     256 (66)     512 (131)
+//   dispatch           1.8 / 2.3    1.9 / 2.4    2.6 / 2.6    3.8 / 3.7
+//   combine            3.2 / 3.5    3.3 / 3.5    3.5 / 3.6    5.3 / 4.2
+// An fp32 buffer into bf16 tokens is even later with 8 slots (256 tokens of
+// 2048, 131 thousand vectors: 3.5 / 4.4) and earlier with 2 (512 tokens of 1024,
+// as many vectors: 2.2 / 2.0).
 constexpr int64_t kFewVectors = 32768;
 
 template <int kU>
@@ -648,7 +659,8 @@ __global__ void __launch_bounds__(kPermThreads) dispatch_kernel(const PermuteArg
 // time are what HBM wants: 512-byte strips with more slots' loads in flight
 // took 66-73 us where these take 52 (8192 tokens, 8 slots, 2048 bf16).  The
 // token's rows and weights are held by lanes, so that no load of a vector
-// waits for one of an index.  kBf16 is the buffer's type, kBf16Out the tokens'.
+// waits for one of an index.  kBf16 is the buffer's type, kBf16Out the tokens':
+// an fp32 buffer (twice the bytes) takes 85 us for the same tokens (6.6 TB/s).
 template <bool kBf16, bool kBf16Out, bool kWeighted, int kU>
 __global__ void __launch_bounds__(kPermThreads, 4) combine_kernel(const PermuteArgs a, int64_t V, int strips) {
   constexpr int N = Vec<kBf16>::kN;
