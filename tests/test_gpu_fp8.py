@@ -757,3 +757,63 @@ def test_wait_limit_of_a_cut_product(api):
         got.fill_(7)
         api.fp8_gemm(a, b, got, ws)
         assert api.averis_check_status(ws) == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("ot", ["f32", "bf16"])
+def test_experts_weight_gradients_of_many_tokens(api, ot):
+    """Experts with more tokens than one visit spans, beside ones with few and
+    none; the rows between hold NaN."""
+    counts, m, n = [7000, 0, 130, 13000, 1], 256, 384
+    assert max(counts) > 2 * 6144
+    E = len(counts)
+    off, cap = _segments(counts)
+    real = torch.zeros(cap, 1, dtype=torch.bool, device="cuda")
+    for o, c in zip(off, counts):
+        real[o:o + c] = True
+    g = torch.Generator(device="cuda").manual_seed(2)
+    nan = torch.full((), float("nan"), device="cuda")
+    X, D = (torch.where(real, torch.randn(cap, c, generator=g, device="cuda") + 0.25, nan).bfloat16() for c in (m, n))
+    ws = api.fp8_moe_workspace(cap, m, n, E)
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    dW, again = (torch.full((E, m, n), 7.0, dtype=DT[ot], device="cuda") for _ in range(2))
+    api.fp8_moe_linear_wgrad(X, D, cnt, dW, ws)
+    api.fp8_moe_linear_wgrad(X, D, cnt, again, ws)
+    assert api.averis_check_status(ws) == 0 and torch.equal(dW, again)
+    for e, (o, c) in enumerate(zip(off, counts)):
+        if c == 0:
+            assert not dW[e].any()
+            continue
+        a, b = (torch.from_numpy(R.deq(t[o:o + c].t().double().cpu().numpy())).cuda() for t in (X, D))
+        ref, mag = a @ b.t(), a.abs() @ b.abs().t()
+        assert ((dW[e].double() - ref).abs() <= c * 2.0 ** -24 * mag + EPS[DT[ot]] * ref.abs()).all()
+        # as in test_gemm_long_sums: a visit's drift, one more rounding for every visit added, and Y's own
+        drift = (192 + 3) * 2.0 ** -24 if ot == "f32" else 192 * 3 * 2.0 ** -24
+        assert ((dW[e].double() - ref).norm() / ref.norm()).item() <= drift + EPS[DT[ot]]
+
+
+def test_more_token_blocks_than_a_grid_dimension_holds(api):
+    """More than 65535 blocks of 128 tokens: the tokens' quantizer against the
+    rows' on the transposed tensor, and a weight gradient over them."""
+    l, K = 65536 * 128 + 5, 16
+    L = -(-l // 128) * 128
+    g = torch.Generator(device="cuda").manual_seed(4)
+    X, D = (torch.randn(l, K, generator=g, device="cuda").bfloat16() for _ in range(2))
+    ws = api.fp8_workspace(l, K, K)
+    t, r = api.FP8Tensor(K, L), api.FP8Tensor(K, L)
+    api.fp8_quant_t(X, t, ws)
+    full = torch.zeros(K, L, dtype=torch.bfloat16, device="cuda")
+    full[:, :l] = X.t()
+    api.fp8_quant(full, r, ws)
+    assert api.averis_check_status(ws) == 0
+    assert torch.equal(t.codes, r.codes) and torch.equal(t.scales, r.scales)
+    dW = torch.empty(K, K, device="cuda")
+    api.fp8_linear_wgrad(X, D, dW, ws)
+    assert api.averis_check_status(ws) == 0
+    full[:, :l] = D.t()
+    api.fp8_quant(full, r, ws)
+    byte = lambda q: torch.from_numpy(R.from_atoms(q.scales.cpu().numpy(), K, L // 128)).cuda()              # noqa: E731
+    value = lambda q: (q.codes.view(torch.float8_e4m3fn).double()                                            # noqa: E731
+                       * torch.exp2(byte(q).double() - 127).repeat_interleave(128, 1))
+    a, b = value(t), value(r)
+    ref, mag = a @ b.t(), a.abs() @ b.abs().t()
+    assert ((dW.double() - ref).abs() <= (192 + L / 6144) * 2.0 ** -24 * mag + 2.0 ** -24 * ref.abs()).all()

@@ -2,6 +2,10 @@
 experts' products (8-bit and NVFP4), combine, and the way back; as one
 captured graph; on two streams at once."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -253,3 +257,27 @@ def test_layer_of_bf16_tokens_rounds_its_outputs_once(api):
     assert api.averis_check_status(layer.ws) == 0
     terms = layer.dY.double().cpu().numpy()[:, None] * Yp.double().cpu().numpy()[layer.row.cpu().numpy()]
     assert np.all(np.abs(layer.dw.double().cpu().numpy() - terms.sum(-1)) <= n * 2.0 ** -24 * np.abs(terms).sum(-1))
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """Nothing has to be run eagerly first but the weights' quantizer: a fresh
+    process captures the layer's calls as its first and replays them."""
+    code = """
+import torch
+from quantized_gemm_column_b200 import api
+from test_gpu_moe_layer import Layer
+torch.zeros(1, device="cuda")
+layer = Layer(api, 60, 6, 2, 256, 128, seed=1)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    layer.forward()
+    layer.backward()
+g.replay()
+layer.check()
+print("captured and replayed")
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([os.path.dirname(here), here]))
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured and replayed" in r.stdout, r.stdout + r.stderr
